@@ -1,9 +1,12 @@
 /*
  * nvfp4_gemv.h -- C ABI of the MI355X (gfx950) NVFP4 g16 W4A16 small-M GEMV
  * library: weight packing, bit-exact dequantisation, the weight-streaming
- * GEMV y[M,N] = x[M,K] . W[N,K]^T for M <= 128 activation rows, and the MoE
+ * GEMV y[M,N] = x[M,K] . W[N,K]^T for M <= 128 activation rows, the MoE
  * expert-slot variant for M <= 8 (gather top-k experts by id, SwiGLU,
- * combine by gate weight).
+ * combine by gate weight), and the parts of a decode step that stand between
+ * these products: RMS norm with the residual, rotary positions with the
+ * append to a paged key-value cache, attention over that cache, and the
+ * verification of drafted tokens.
  *
  * The operations are the ones the GLM-5.3-Flash-NVFP4 blueprint pages
  * describe for their decode step:
@@ -471,6 +474,253 @@ nvfp4_status nvfp4_moe_gemv_noalloc(const uint8_t* w13_codes, const uint8_t* w13
                                     const uint16_t* x, const int32_t* expert_ids,
                                     const float* gate_w, int64_t M, int64_t E, int64_t H,
                                     int64_t I, int64_t topk, float* y, hipStream_t stream);
+
+/* Element types of the arrays whose type a call lets the caller choose. */
+typedef enum nvfp4_dtype {
+  NVFP4_BF16 = 0, /* bf16 bit patterns (uint16) */
+  NVFP4_F32 = 1,
+  NVFP4_E4M3 = 2  /* OCP E4M3FN bytes */
+} nvfp4_dtype;
+
+/* Largest number of rows (tokens) of one norm or rotation call. */
+#define NVFP4_MAX_ROWS (1 << 21)
+/* Largest row length H of one norm call. */
+#define NVFP4_NORM_MAX_H (1 << 15)
+
+/*
+ * nvfp4_add_rmsnorm -- RMS norm with the residual's addition, in front of a
+ * GEMV:
+ *
+ *   s[m, i]            = x[m, i] + residual[m, i]            (fp32)
+ *   residual_out[m, i] = s[m, i]                             (rounded once)
+ *   y[m, i]            = s[m, i] * rsqrt(mean_i s[m, i]^2 + eps) * weight[i]
+ *
+ * y comes from the fp32 s, not from its rounding, and is rounded once to bf16
+ * (nvfp4_gemv's x). All sums are fp32, in an order that H alone fixes.
+ *
+ *   x             bf16 or fp32 (x_type NVFP4_BF16 / NVFP4_F32, a GEMV's y)
+ *                 [M, H], 16-byte aligned;
+ *   residual      bf16 or fp32 (residual_type) [M, H], 16-byte aligned, or
+ *                 NULL: s = x, and residual_out must be NULL too;
+ *   residual_out  [M, H] out, the type of residual; may be residual itself
+ *                 (in place), must not overlap it otherwise;
+ *   weight        bf16[H], 16-byte aligned;  eps  finite, >= 0;
+ *   M             0 <= M <= NVFP4_MAX_ROWS;
+ *   H             0 <= H <= NVFP4_NORM_MAX_H, H % 8 == 0;
+ *   y             bf16[M, H] out, 16-byte aligned.
+ * Errors: NULL, SHAPE (a type that is not allowed and eps included), ALIGN,
+ * UNSUPPORTED, ALIAS, HIP.
+ */
+nvfp4_status nvfp4_add_rmsnorm(const void* x, int x_type, const void* residual,
+                               void* residual_out, int residual_type, const uint16_t* weight,
+                               float eps, int64_t M, int64_t H, uint16_t* y, hipStream_t stream);
+
+/*
+ * nvfp4_add_rmsnorm_e4m3 -- nvfp4_add_rmsnorm with an 8-bit output: for every
+ * run of `group` elements of a row (the whole row where group is 0)
+ *
+ *   scale = max|y| / 448  (1 where that is 0),  y8 = E4M3(y / scale)
+ *
+ * with y in fp32 (IEEE divisions, round to nearest even, saturating).
+ *
+ *   group   0, 32, 64 or 128, dividing H;
+ *   y8      uint8[M, H] out, 8-byte aligned;
+ *   scales  float[M, group ? H / group : 1] out.
+ * Everything else as nvfp4_add_rmsnorm.
+ */
+nvfp4_status nvfp4_add_rmsnorm_e4m3(const void* x, int x_type, const void* residual,
+                                    void* residual_out, int residual_type,
+                                    const uint16_t* weight, float eps, int64_t M, int64_t H,
+                                    int64_t group, uint8_t* y8, float* scales,
+                                    hipStream_t stream);
+
+/*
+ * nvfp4_add_rmsnorm_nvfp4 -- nvfp4_add_rmsnorm with the NVFP4 output that
+ * nvfp4_gemv_w4a4 reads: the quantisation of nvfp4_quantize_act with the
+ * static scale *gscale, taken from the fp32 y (not from its bf16 rounding).
+ *
+ *   gscale  float[1], > 0 and finite (device data, not checked);
+ *   codes   uint8[M, H/2] out, 8-byte aligned; scales uint8[M, H/16] out;
+ *   H % 32 == 0.
+ * Everything else as nvfp4_add_rmsnorm; s has to be finite.
+ */
+nvfp4_status nvfp4_add_rmsnorm_nvfp4(const void* x, int x_type, const void* residual,
+                                     void* residual_out, int residual_type,
+                                     const uint16_t* weight, float eps, int64_t M, int64_t H,
+                                     const float* gscale, uint8_t* codes, uint8_t* scales,
+                                     hipStream_t stream);
+
+/*
+ * nvfp4_kv_cache -- a paged key-value cache: num_blocks pages of `page`
+ * tokens, each with n_kv_heads keys and values of D elements.
+ *
+ *   k, v          element (block, token, head, d) of both lies at block *
+ *                 stride_block + token * stride_token + head * stride_head +
+ *                 d; so [blocks, page, heads, D] and [blocks, heads, page, D]
+ *                 and pages that hold k next to v are all fine. 16-byte
+ *                 aligned, strides >= D and multiples of 16 bytes,
+ *                 stride_token < 2^26; no two elements may share an address
+ *                 (not checked);
+ *   type          NVFP4_BF16, or NVFP4_E4M3: an element stands for its value
+ *                 times *k_scale (*v_scale), device float[1], > 0 and finite
+ *                 (not checked; ignored for bf16);
+ *   page          1 <= page <= 2^20;  num_blocks  0 <= num_blocks < 2^31.
+ * The structure is read on the host during the call.
+ */
+typedef struct nvfp4_kv_cache {
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t num_blocks, page, n_kv_heads, D;
+  int64_t stride_block, stride_token, stride_head;
+  int type;
+} nvfp4_kv_cache;
+
+/* Largest number of query or key-value heads. */
+#define NVFP4_MAX_HEADS 1024
+/* Largest head dimension D of nvfp4_rope_append. */
+#define NVFP4_ROPE_MAX_D 512
+
+/*
+ * nvfp4_rope_append -- rotary positions of q and k, and the append of k and v
+ * to a paged cache, in one pass. Pair i < R / 2 of the first R elements of a
+ * head turns by a = positions[t] * inv_freq[i]:
+ *
+ *   (x0, x1) -> (x0 cos a - x1 sin a, x1 cos a + x0 sin a) * rope_scale
+ *
+ * where x0, x1 are elements i and i + R / 2 (interleaved 0) or 2 i and 2 i + 1
+ * (interleaved 1); elements R .. D - 1, and v, stay as they are. Contexts are
+ * scaled through inv_freq (the caller's table, computed once) and rope_scale.
+ * The angle is formed and reduced in 64 bits, the rest is fp32, rounded once.
+ *
+ *   q, k, v      bf16 or fp32 (x_type) [T, heads, D]; a token's heads are
+ *                contiguous, tokens lie *_stride elements apart (so the three
+ *                may be views of one projection's output), 16-byte aligned;
+ *                q may be NULL with Hq == 0 (only append), k and v NULL with
+ *                cache NULL (only rotate q);
+ *   positions    int64[T];
+ *   slots        int64[T]: token t goes to page slots[t] / page, place
+ *                slots[t] % page; a slot outside the cache (a negative one:
+ *                padding) is not written. The slots inside it must differ
+ *                from each other (otherwise which token's elements stay is
+ *                not defined);
+ *   inv_freq     float[R / 2];  rope_scale  finite;
+ *   D, R         multiples of 16, 16 <= D <= NVFP4_ROPE_MAX_D, 0 <= R <= D
+ *                (D and the number of key-value heads are the cache's where
+ *                there is one);
+ *   q_out        bf16[T, Hq, D] out, 16-byte aligned;
+ *   cache        as above; an E4M3 cache gets E4M3(x / scale), saturating.
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, ALIAS, HIP.
+ */
+nvfp4_status nvfp4_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                               const void* v, int64_t v_stride, int x_type,
+                               const int64_t* positions, const int64_t* slots,
+                               const float* inv_freq, int64_t T, int64_t Hq, int64_t D,
+                               int64_t R, int interleaved, float rope_scale, uint16_t* q_out,
+                               const nvfp4_kv_cache* cache, hipStream_t stream);
+
+/* Largest number of sequences, and of new tokens per sequence, of one
+   nvfp4_paged_attention call. */
+#define NVFP4_ATTN_MAX_B 4096
+#define NVFP4_ATTN_MAX_Q 64
+
+/*
+ * nvfp4_paged_attention_workspace_bytes -- device workspace that
+ * nvfp4_paged_attention needs: the partial sums of the workgroups that share a
+ * sequence and head. It does not grow with the lengths. 0 for sizes that the
+ * call refuses.
+ */
+size_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv,
+                                             int64_t D);
+
+/*
+ * nvfp4_paged_attention -- attention of the Q newest tokens of each of B
+ * sequences over a paged cache that holds them too (nvfp4_rope_append): token
+ * i of sequence b sits at position p = seq_lens[b] - Q + i and sees the keys
+ * 0 .. p (with a window > 0: the last `window` of them, p included):
+ *
+ *   out[b, i, h] = sum_j softmax_j(scale * q[b, i, h] . K[j, h / G]) V[j, h / G]
+ *
+ * with G = Hq / Hkv. A token that sees no key (seq_lens[b] <= 0, or p < 0)
+ * gives zeros. A key or value that a token does not see does not reach it,
+ * whatever its bits are (NaN and infinities included). Scores, maxima and
+ * sums are fp32; the probabilities are rounded to bf16 for the product with V.
+ *
+ *   q            bf16[B * Q, Hq, D] (uint16 bits), 16-byte aligned;
+ *   cache        bf16 or E4M3, D 64, 128 or 256;
+ *   block_table  int32[B, max_blocks]: page j of sequence b holds its keys
+ *                j * page .. A number outside [0, num_blocks) hides its keys;
+ *                entries past a sequence's last page are not used;
+ *   seq_lens     int32[B], the new tokens included; more than max_blocks *
+ *                page counts as that;
+ *   scale        the scores' factor, usually 1 / sqrt(D);
+ *   B, Q         0 <= B <= NVFP4_ATTN_MAX_B, 0 <= Q <= NVFP4_ATTN_MAX_Q;
+ *   Hq           a multiple of the cache's n_kv_heads, <= NVFP4_MAX_HEADS;
+ *   out          bf16[B * Q, Hq, D] out, 16-byte aligned;
+ *   workspace    at least nvfp4_paged_attention_workspace_bytes(B, Q, Hq, Hkv,
+ *                D) bytes, 256-byte aligned; overwritten, its content does
+ *                not matter; must not be shared by calls that may run
+ *                concurrently.
+ * One launch, or two where a sequence may be longer than 128 keys. The work is
+ * divided on the device by the lengths, so a captured call follows them.
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, WORKSPACE, ALIAS, HIP.
+ */
+nvfp4_status nvfp4_paged_attention(const uint16_t* q, const nvfp4_kv_cache* cache,
+                                   const int32_t* block_table, const int32_t* seq_lens,
+                                   int64_t B, int64_t Q, int64_t Hq, int64_t max_blocks,
+                                   float scale, int64_t window, uint16_t* out, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
+
+/* Largest number of drafts per sequence, of sequences and of vocabulary
+   entries of one nvfp4_verify_draft call. */
+#define NVFP4_VERIFY_MAX_Q 63
+#define NVFP4_VERIFY_MAX_B 4096
+#define NVFP4_VERIFY_MAX_V (1 << 24)
+
+/*
+ * nvfp4_verify_draft_workspace_bytes -- device workspace of
+ * nvfp4_verify_draft: partial sums of each sequence's row. 0 for sizes that
+ * the call refuses.
+ */
+size_t nvfp4_verify_draft_workspace_bytes(int64_t B, int64_t V);
+
+/*
+ * nvfp4_verify_draft -- speculative verification from given random numbers.
+ * For each sequence, with p = target_p[b], q = draft_p[b], d = draft[b]:
+ *
+ *   n = the first j with  not  u_accept[b, j] * q[j, d_j] < p[j, d_j]
+ *       (n = n_draft[b] if there is none),
+ *   r = max(p[n] - q[n], 0) if n < n_draft[b] (p[n] if that is zero
+ *       everywhere), else p[n],
+ *   t = the lowest v with  sum_{i <= v} r_i > u_sample[b] * sum_i r_i
+ *       (V - 1 if there is none),
+ *   tokens[b] = d_0 .. d_{n-1}, t, -1 ..;   n_accepted[b] = n.
+ *
+ * Without draft_p the drafts are certain: q[j] is 1 at d_j and 0 elsewhere,
+ * and r is p with entry d_n taken out. A draft outside [0, V) is not accepted. All products
+ * and sums are 64-bit, in a fixed order.
+ *
+ *   target_p    float[B, Q + 1, V], >= 0;  draft_p float[B, Q, V] or NULL;
+ *   draft       int32[B, Q];  n_draft int32[B] (how many of them are real;
+ *               taken into 0 .. Q) or NULL: Q for all;
+ *   u_accept    float[B, Q], u_sample float[B]: in [0, 1);
+ *   B, Q, V     0 <= B <= NVFP4_VERIFY_MAX_B, 0 <= Q <= NVFP4_VERIFY_MAX_Q
+ *               (draft, draft_p and u_accept may be NULL at Q == 0),
+ *               1 <= V <= NVFP4_VERIFY_MAX_V;
+ *   tokens      int32[B, Q + 1] out;  n_accepted int32[B] out;
+ *   workspace   at least nvfp4_verify_draft_workspace_bytes(B, V) bytes,
+ *               256-byte aligned; overwritten; must not be shared by calls
+ *               that may run concurrently.
+ * Every pointer is 4-byte aligned. Probabilities that are NaN, infinite or
+ * negative give an unspecified token inside [0, V).
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, WORKSPACE, ALIAS, HIP.
+ */
+nvfp4_status nvfp4_verify_draft(const float* target_p, const float* draft_p, const int32_t* draft,
+                                const int32_t* n_draft, const float* u_accept,
+                                const float* u_sample, int64_t B, int64_t Q, int64_t V,
+                                int32_t* tokens, int32_t* n_accepted, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
 
 /*
  * nvfp4_stream_read -- measurement aid, not part of the product path: reads

@@ -18,6 +18,13 @@ Functions (same names as the C entry points, without the prefix):
   moe_shared_workspace_bytes(M, H, I, topk, I_shared) -> int
   moe_shared_gemv(w13..., w2..., x, ids, gate_w, shared[, workspace]) -> y
   moe_gemv_noalloc_into(w13..., w2..., x, ids, gate_w, y)  (no workspace)
+  add_rmsnorm(x, weight, eps[, residual])         -> y (bf16), residual_out
+  add_rmsnorm_e4m3(x, weight, eps[, residual, group]) -> y8, scales, residual_out
+  add_rmsnorm_nvfp4(x, weight, eps, gscale[, residual]) -> codes, scales, residual_out
+  rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, ...) -> q_out (bf16)
+  paged_attention(q, k_cache, v_cache, block_table, seq_lens, ...) -> out (bf16)
+  verify_draft(target_p, draft_p, draft, u_accept, u_sample, ...) -> tokens, n_accepted
+  paged_attention_workspace_bytes(B, Q, Hq, Hkv, D), verify_draft_workspace_bytes(B, V)
   stream_read(buf, sink)                 (measurement aid: one pure read of buf)
 The ``*_into`` variants write into caller-provided outputs.
 """
@@ -43,6 +50,17 @@ MAX_N = 1 << 30
 MAX_K = 1 << 20
 MOE_MAX_I = 1 << 24
 MOE_MAX_H = 1 << 24
+# NVFP4_MAX_ROWS, NVFP4_NORM_MAX_H, NVFP4_MAX_HEADS, NVFP4_ROPE_MAX_D,
+# NVFP4_ATTN_MAX_B, NVFP4_ATTN_MAX_Q, NVFP4_VERIFY_MAX_Q / _B / _V.
+MAX_ROWS = 1 << 21
+NORM_MAX_H = 1 << 15
+MAX_HEADS = 1024
+ROPE_MAX_D = 512
+ATTN_MAX_B = 4096
+ATTN_MAX_Q = 64
+VERIFY_MAX_Q = 63
+VERIFY_MAX_B = 4096
+VERIFY_MAX_V = 1 << 24
 # NVFP4_NOALLOC_SCRATCH_BYTES: the device array of nvfp4_moe_gemv_noalloc.
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
@@ -72,6 +90,21 @@ class MoeShared(ctypes.Structure):
                 ("w13_gscale", ctypes.c_void_p), ("w2_codes", ctypes.c_void_p),
                 ("w2_scales", ctypes.c_void_p), ("w2_gscale", ctypes.c_void_p),
                 ("I", ctypes.c_int64)]
+
+
+class KvCache(ctypes.Structure):
+    """nvfp4_kv_cache: a paged key-value cache."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("num_blocks", ctypes.c_int64),
+                ("page", ctypes.c_int64), ("n_kv_heads", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("stride_block", ctypes.c_int64), ("stride_token", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("type", ctypes.c_int)]
+
+
+# nvfp4_dtype
+_BF16, _F32, _E4M3 = 0, 1, 2
+_ACT_TYPES = {torch.bfloat16: _BF16, torch.float32: _F32}
+_CACHE_TYPES = {torch.bfloat16: _BF16, torch.float8_e4m3fn: _E4M3}
 
 
 def lib() -> ctypes.CDLL:
@@ -125,6 +158,28 @@ def lib() -> ctypes.CDLL:
                                            ctypes.c_size_t, _VP])
         L.nvfp4_moe_gemv_noalloc.restype = ctypes.c_int
         L.nvfp4_moe_gemv_noalloc.argtypes = [_VP] * 9 + [_I64] * 5 + [_VP, _VP]
+        norm = [_VP, ctypes.c_int, _VP, _VP, ctypes.c_int, _VP, ctypes.c_float, _I64, _I64]
+        L.nvfp4_add_rmsnorm.restype = ctypes.c_int
+        L.nvfp4_add_rmsnorm.argtypes = norm + [_VP, _VP]
+        L.nvfp4_add_rmsnorm_e4m3.restype = ctypes.c_int
+        L.nvfp4_add_rmsnorm_e4m3.argtypes = norm + [_I64, _VP, _VP, _VP]
+        L.nvfp4_add_rmsnorm_nvfp4.restype = ctypes.c_int
+        L.nvfp4_add_rmsnorm_nvfp4.argtypes = norm + [_VP] * 4
+        L.nvfp4_rope_append.restype = ctypes.c_int
+        L.nvfp4_rope_append.argtypes = ([_VP, _I64] * 3 + [ctypes.c_int] + [_VP] * 3 +
+                                        [_I64] * 4 + [ctypes.c_int, ctypes.c_float, _VP,
+                                                      ctypes.POINTER(KvCache), _VP])
+        L.nvfp4_paged_attention_workspace_bytes.restype = ctypes.c_size_t
+        L.nvfp4_paged_attention_workspace_bytes.argtypes = [_I64] * 5
+        L.nvfp4_paged_attention.restype = ctypes.c_int
+        L.nvfp4_paged_attention.argtypes = [_VP, ctypes.POINTER(KvCache), _VP, _VP, _I64, _I64,
+                                            _I64, _I64, ctypes.c_float, _I64, _VP, _VP,
+                                            ctypes.c_size_t, _VP]
+        L.nvfp4_verify_draft_workspace_bytes.restype = ctypes.c_size_t
+        L.nvfp4_verify_draft_workspace_bytes.argtypes = [_I64, _I64]
+        L.nvfp4_verify_draft.restype = ctypes.c_int
+        L.nvfp4_verify_draft.argtypes = [_VP] * 6 + [_I64] * 3 + [_VP] * 3 + [ctypes.c_size_t,
+                                                                             _VP]
         L.nvfp4_stream_read.restype = ctypes.c_int
         L.nvfp4_stream_read.argtypes = [_VP, ctypes.c_size_t, _VP, _VP]
         L.nvfp4_check_device_faults.restype = ctypes.c_int
@@ -565,3 +620,292 @@ def moe_w4a4_workspace_layout(M: int, H: int, I: int, topk: int, I_shared: int =
     hq = a(hs + M * I_shared * 2)
     xq = a(hq + M * topk * I * 2)
     return {"h": 0, "hs": hs, "hq": hq, "xq": xq, "total": a(xq + M * H * 2)}
+
+
+# ------------------------------------------------- between the GEMVs: norms
+
+def _norm_args(x, weight, residual, residual_out, *outs):
+    """The arguments that the three norms share, checked."""
+    _dev(x, weight, residual, residual_out, *outs)
+    xt = _ACT_TYPES.get(x.dtype)
+    if xt is None or weight.dtype is not torch.bfloat16:
+        raise TypeError(f"x must be bf16 or fp32 and weight bf16, got {x.dtype}, {weight.dtype}")
+    M, H = x.shape
+    if weight.shape != (H,):
+        raise ValueError(f"weight must have shape ({H},), got {tuple(weight.shape)}")
+    if (residual is None) != (residual_out is None):
+        raise ValueError("residual and residual_out go together")
+    if residual is None:
+        return x.data_ptr(), xt, None, None, 0, weight.data_ptr(), M, H
+    rt = _ACT_TYPES.get(residual.dtype)
+    if rt is None or residual_out.dtype is not residual.dtype:
+        raise TypeError("residual must be bf16 or fp32, residual_out the same")
+    if residual.shape != x.shape or residual_out.shape != x.shape:
+        raise ValueError("residual and residual_out must have x's shape")
+    return (x.data_ptr(), xt, residual.data_ptr(), residual_out.data_ptr(), rt,
+            weight.data_ptr(), M, H)
+
+
+def add_rmsnorm_into(x, weight, eps, y, residual=None, residual_out=None) -> None:
+    """y[M, H] (bf16) = s rsqrt(mean s^2 + eps) weight with s = x + residual,
+    which goes to residual_out (may be residual itself). x is bf16 or fp32
+    (a GEMV's output), so is the residual."""
+    *a, M, H = _norm_args(x, weight, residual, residual_out, y)
+    if y.dtype is not torch.bfloat16 or y.shape != x.shape:
+        raise ValueError("y must be bf16 and have x's shape")
+    _check("nvfp4_add_rmsnorm", lib().nvfp4_add_rmsnorm(*a, eps, M, H, y.data_ptr(), _stream(x)))
+
+
+def add_rmsnorm(x, weight, eps, residual=None):
+    """(y, residual_out); residual_out is None without a residual."""
+    y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    r = None if residual is None else torch.empty_like(residual)
+    add_rmsnorm_into(x, weight, eps, y, residual, r)
+    return y, r
+
+
+def add_rmsnorm_e4m3_into(x, weight, eps, y8, scales, residual=None, residual_out=None) -> None:
+    """add_rmsnorm_into with y8 (float8_e4m3fn [M, H]) and scales fp32
+    [M, H / group]: groups of 32, 64 or 128, or a whole row ([M, 1])."""
+    *a, M, H = _norm_args(x, weight, residual, residual_out, y8, scales)
+    if y8.dtype is not torch.float8_e4m3fn or scales.dtype is not torch.float32 \
+            or y8.shape != x.shape or scales.dim() != 2 or scales.shape[0] != M:
+        raise ValueError("y8 must be float8_e4m3fn with x's shape, scales fp32 [M, H / group]")
+    n = scales.shape[1]
+    if n < 1 or H % n:
+        raise ValueError(f"scales has {n} columns, which do not divide H = {H}")
+    group = 0 if n == 1 else H // n
+    _check("nvfp4_add_rmsnorm_e4m3", lib().nvfp4_add_rmsnorm_e4m3(
+        *a, eps, M, H, group, y8.data_ptr(), scales.data_ptr(), _stream(x)))
+
+
+def add_rmsnorm_e4m3(x, weight, eps, residual=None, group: int = 0):
+    """(y8, scales, residual_out)."""
+    M, H = x.shape
+    y8 = torch.empty((M, H), dtype=torch.float8_e4m3fn, device=x.device)
+    scales = torch.empty((M, H // group if group else 1), dtype=torch.float32, device=x.device)
+    r = None if residual is None else torch.empty_like(residual)
+    add_rmsnorm_e4m3_into(x, weight, eps, y8, scales, residual, r)
+    return y8, scales, r
+
+
+def add_rmsnorm_nvfp4_into(x, weight, eps, gscale, codes, scales, residual=None,
+                           residual_out=None) -> None:
+    """add_rmsnorm_into with the NVFP4 activations of gemv_w4a4 (static input
+    scale gscale, fp32 [1]): codes u8[M, H/2], scales u8[M, H/16]."""
+    *a, M, H = _norm_args(x, weight, residual, residual_out, gscale, codes, scales)
+    if gscale.dtype is not torch.float32 or codes.dtype is not torch.uint8 \
+            or scales.dtype is not torch.uint8 or codes.shape != (M, H // 2) \
+            or scales.shape != (M, H // 16):
+        raise ValueError("gscale must be fp32 [1], codes u8 [M, H/2], scales u8 [M, H/16]")
+    _check("nvfp4_add_rmsnorm_nvfp4", lib().nvfp4_add_rmsnorm_nvfp4(
+        *a, eps, M, H, gscale.data_ptr(), codes.data_ptr(), scales.data_ptr(), _stream(x)))
+
+
+def add_rmsnorm_nvfp4(x, weight, eps, gscale, residual=None):
+    """(codes, scales, residual_out)."""
+    M, H = x.shape
+    codes = torch.empty((M, H // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((M, H // 16), dtype=torch.uint8, device=x.device)
+    r = None if residual is None else torch.empty_like(residual)
+    add_rmsnorm_nvfp4_into(x, weight, eps, gscale, codes, scales, residual, r)
+    return codes, scales, r
+
+
+# -------------------------------------------- between the GEMVs: attention
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale) -> KvCache:
+    """The descriptor of caches [blocks, page, heads, D] (any strides with
+    contiguous elements, the same for both)."""
+    ct = _CACHE_TYPES.get(k_cache.dtype)
+    if ct is None or v_cache.dtype is not k_cache.dtype:
+        raise TypeError("the caches must both be bf16 or float8_e4m3fn")
+    st = k_cache.stride()
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.stride() != st \
+            or st[3] != 1:
+        raise ValueError("the caches must have one shape [blocks, page, heads, D] and the same "
+                         "strides, the last one 1")
+    nb, page, heads, D = k_cache.shape
+    if ct == _E4M3:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
+            raise TypeError("k_scale and v_scale must be fp32 [1]")
+        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
+    else:
+        ks = vs = None
+    # the stride of a dimension of one says nothing
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, nb, page, heads, D,
+                   st[0] if nb > 1 else D, st[1] if page > 1 else D, st[2] if heads > 1 else D,
+                   ct)
+
+
+def _same_device(d, *ts):
+    """Tensors (None is skipped) on the HIP device of index d."""
+    for t in ts:
+        if t is not None and (not t.is_cuda or t.get_device() != d):
+            raise ValueError("tensors must be on one HIP device")
+
+
+def rope_append_into(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache, k_scale=None,
+                     v_scale=None, interleaved: bool = False, rope_scale: float = 1.0) -> None:
+    """Rotary positions of q[T, Hq, D] and k[T, Hkv, D] (bf16 or fp32; a
+    token's heads contiguous, tokens at any stride, so views of one fused
+    projection), q to q_out (bf16 [T, Hq, D]), k and v into the pages
+    k_cache, v_cache[blocks, page, Hkv, D] at slots (int64 [T], page number *
+    page size + place; outside the cache: not written). positions int64 [T];
+    inv_freq fp32 [R / 2] turns the first R elements of each head. q and q_out
+    may be None (only append); k, v, slots and the caches may be (only
+    rotate)."""
+    x = k if q is None else q
+    if x is None:
+        raise ValueError("neither q nor k is given")
+    d = x.get_device()
+    _same_device(d, q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache, k_scale, v_scale)
+    xt = _ACT_TYPES.get(x.dtype)
+    if xt is None:
+        raise TypeError(f"q, k and v must be bf16 or fp32, got {x.dtype}")
+    T, _, D = x.shape
+    if positions.dtype is not torch.int64 or positions.shape != (T,) \
+            or not positions.is_contiguous():
+        raise ValueError("positions must be contiguous int64 [T]")
+    if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be contiguous fp32 [R / 2]")
+    qp = qs = op = kp = ks = vp = vs = sp = cache = None
+    Hq = 0
+    if q is not None:
+        Hq, st = q.shape[1], q.stride()
+        if st[2] != 1 or (st[1] != D and Hq > 1):
+            raise ValueError("the heads of a token of q must be contiguous")
+        if q_out is None or q_out.dtype is not torch.bfloat16 or q_out.shape != q.shape \
+                or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous bf16 with q's shape")
+        qp, qs, op = q.data_ptr(), st[0], q_out.data_ptr()
+        if T == 1:   # one token's stride says nothing
+            qs = Hq * D
+    if k is not None:
+        c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+        Hkv, st, sv = c.n_kv_heads, k.stride(), v.stride()
+        if k.dtype is not x.dtype or v.dtype is not x.dtype or k.shape != (T, Hkv, D) \
+                or v.shape != k.shape or c.D != D:
+            raise ValueError(f"k and v must be {x.dtype} [{T}, {Hkv}, {c.D}], got "
+                             f"{tuple(k.shape)}, {tuple(v.shape)}")
+        if st[2] != 1 or sv[2] != 1 or ((st[1] != D or sv[1] != D) and Hkv > 1):
+            raise ValueError("the heads of a token of k and v must be contiguous")
+        if slots is None or slots.dtype is not torch.int64 or slots.shape != (T,) \
+                or not slots.is_contiguous():
+            raise ValueError("slots must be contiguous int64 [T]")
+        kp, ks, vp, vs, sp = k.data_ptr(), st[0], v.data_ptr(), sv[0], slots.data_ptr()
+        if T == 1:
+            ks = vs = Hkv * D
+        cache = ctypes.byref(c)
+    _check("nvfp4_rope_append", lib().nvfp4_rope_append(
+        qp, qs or 0, kp, ks or 0, vp, vs or 0, xt, positions.data_ptr(), sp,
+        inv_freq.data_ptr(), T, Hq, D, 2 * inv_freq.shape[0], 1 if interleaved else 0,
+        rope_scale, op, cache, _stream(x)))
+
+
+def rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, k_scale=None, v_scale=None,
+                interleaved: bool = False, rope_scale: float = 1.0):
+    """q_out (bf16 [T, Hq, D]; None without q)."""
+    q_out = None if q is None else torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    rope_append_into(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache, k_scale,
+                     v_scale, interleaved, rope_scale)
+    return q_out
+
+
+def paged_attention_workspace_bytes(B: int, Q: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().nvfp4_paged_attention_workspace_bytes(B, Q, Hq, Hkv, D))
+
+
+def paged_attention_into(q, k_cache, v_cache, block_table, seq_lens, out, workspace,
+                         scale: float | None = None, window: int = 0, k_scale=None,
+                         v_scale=None) -> None:
+    """Attention of the T / B newest tokens of each of B sequences over pages
+    k_cache, v_cache[blocks, page, Hkv, D] (bf16, or e4m3 with k_scale,
+    v_scale fp32 [1]). q and out bf16 [T, Hq, D], sequence by sequence;
+    block_table int32 [B, max_blocks]; seq_lens int32 [B], the new tokens
+    included; scale defaults to D ** -0.5; window > 0: each token sees the
+    last `window` keys up to itself."""
+    d = q.get_device()
+    _same_device(d, q, k_cache, v_cache, block_table, seq_lens, out, workspace, k_scale, v_scale)
+    if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 \
+            or block_table.dtype is not torch.int32 or seq_lens.dtype is not torch.int32:
+        raise TypeError("q and out must be bf16, block_table and seq_lens int32")
+    if not (q.is_contiguous() and out.is_contiguous() and block_table.is_contiguous()
+            and seq_lens.is_contiguous() and workspace.is_contiguous()):
+        raise ValueError("q, out, block_table, seq_lens and workspace must be contiguous")
+    c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    T, Hq, D = q.shape
+    B, width = block_table.shape
+    if seq_lens.shape != (B,) or out.shape != q.shape or D != c.D or (T % B if B else T):
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, out {tuple(out.shape)}, "
+                         f"block_table {tuple(block_table.shape)}, seq_lens "
+                         f"{tuple(seq_lens.shape)}, D {c.D}")
+    _check("nvfp4_paged_attention", lib().nvfp4_paged_attention(
+        q.data_ptr(), ctypes.byref(c), block_table.data_ptr(), seq_lens.data_ptr(), B,
+        T // B if B else 0, Hq, width, D ** -0.5 if scale is None else scale, window,
+        out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _stream(q)))
+
+
+def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale: float | None = None,
+                    window: int = 0, k_scale=None, v_scale=None,
+                    workspace: torch.Tensor | None = None) -> torch.Tensor:
+    T, Hq, D = q.shape
+    B = block_table.shape[0]
+    if workspace is None:
+        n = paged_attention_workspace_bytes(B, T // B if B else 0, Hq, k_cache.shape[2], D)
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    out = torch.empty_like(q)
+    paged_attention_into(q, k_cache, v_cache, block_table, seq_lens, out, workspace, scale,
+                         window, k_scale, v_scale)
+    return out
+
+
+# ------------------------------------------------- after the LM head: drafts
+
+def verify_draft_workspace_bytes(B: int, V: int) -> int:
+    return int(lib().nvfp4_verify_draft_workspace_bytes(B, V))
+
+
+def verify_draft_into(target_p, draft_p, draft, u_accept, u_sample, tokens, n_accepted, workspace,
+                      n_draft=None) -> None:
+    """Speculative verification: target_p fp32 [B, Q + 1, V], draft_p fp32
+    [B, Q, V] (None: the drafts are certain), draft int32 [B, Q], u_accept
+    fp32 [B, Q] and u_sample fp32 [B] in [0, 1); n_draft int32 [B]: how many
+    of the drafts are real (None: all). tokens int32 [B, Q + 1]: the kept
+    drafts, the token drawn after them, then -1; n_accepted int32 [B]."""
+    _dev(target_p, draft_p, draft, u_accept, u_sample, tokens, n_accepted, workspace, n_draft)
+    f, i = torch.float32, torch.int32
+    if target_p.dtype is not f or (draft_p is not None and draft_p.dtype is not f) \
+            or u_accept.dtype is not f or u_sample.dtype is not f or draft.dtype is not i \
+            or tokens.dtype is not i or n_accepted.dtype is not i \
+            or (n_draft is not None and n_draft.dtype is not i):
+        raise TypeError("probabilities and u must be fp32, draft, tokens, n_accepted and n_draft "
+                        "int32")
+    B, Q1, V = target_p.shape
+    Q = Q1 - 1
+    if draft.shape != (B, Q) or u_accept.shape != (B, Q) or u_sample.shape != (B,) \
+            or tokens.shape != (B, Q1) or n_accepted.shape != (B,) \
+            or (draft_p is not None and draft_p.shape != (B, Q, V)) \
+            or (n_draft is not None and n_draft.shape != (B,)):
+        raise ValueError(f"shapes do not fit target_p {tuple(target_p.shape)}")
+    _check("nvfp4_verify_draft", lib().nvfp4_verify_draft(
+        target_p.data_ptr(), _p(draft_p), draft.data_ptr(), _p(n_draft), u_accept.data_ptr(),
+        u_sample.data_ptr(), B, Q, V, tokens.data_ptr(), n_accepted.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(target_p)))
+
+
+def verify_draft(target_p, draft_p, draft, u_accept, u_sample, n_draft=None,
+                 workspace: torch.Tensor | None = None):
+    """(tokens, n_accepted)."""
+    B, Q1, V = target_p.shape
+    if workspace is None:
+        workspace = torch.empty(max(verify_draft_workspace_bytes(B, V), 256), dtype=torch.uint8,
+                                device=target_p.device)
+    tokens = torch.empty((B, Q1), dtype=torch.int32, device=target_p.device)
+    n_accepted = torch.empty((B,), dtype=torch.int32, device=target_p.device)
+    verify_draft_into(target_p, draft_p, draft, u_accept, u_sample, tokens, n_accepted, workspace,
+                      n_draft)
+    return tokens, n_accepted

@@ -380,6 +380,447 @@ nvfp4_status nvfp4_gemv_w4a4_segments(const nvfp4_gemv_segment* segs, int64_t n_
                     "nvfp4_gemv_w4a4_segments launch");
 }
 
+namespace {
+
+// The checks that the three norm entry points share. `y` (yb bytes, aligned to
+// ya) and `extra` (eb bytes, an output, 4-byte aligned) are theirs; extra_in:
+// a float[1] input.
+nvfp4_status norm_checks(const char* fn, const void* x, int x_type, const void* residual,
+                         void* residual_out, int residual_type, const uint16_t* weight,
+                         float eps, int64_t M, int64_t H, int64_t unit, const void* y, size_t yb,
+                         size_t ya, const void* extra, size_t eb, size_t ea,
+                         const float* extra_in, nvfp4::NormArgs* a, bool* nothing) {
+  *nothing = false;
+  if (M < 0 || H < 0 || H % unit != 0)
+    return fail(NVFP4_ERR_SHAPE, "%s: need M, H >= 0 and H %% %lld == 0 (M=%lld H=%lld)", fn,
+                (long long)unit, (long long)M, (long long)H);
+  if ((x_type != NVFP4_BF16 && x_type != NVFP4_F32) ||
+      (residual && residual_type != NVFP4_BF16 && residual_type != NVFP4_F32))
+    return fail(NVFP4_ERR_SHAPE, "%s: x and residual are bf16 or fp32 (types %d, %d)", fn, x_type,
+                residual_type);
+  if (!(eps >= 0.0f) || eps > 3.0e38f)
+    return fail(NVFP4_ERR_SHAPE, "%s: eps must be finite and >= 0", fn);
+  if (M > NVFP4_MAX_ROWS || H > NVFP4_NORM_MAX_H)
+    return fail(NVFP4_ERR_UNSUPPORTED, "%s: M=%lld (max %d), H=%lld (max %d)", fn, (long long)M,
+                NVFP4_MAX_ROWS, (long long)H, NVFP4_NORM_MAX_H);
+  if (M == 0 || H == 0) {
+    *nothing = true;
+    return NVFP4_OK;
+  }
+  if (!x || !weight || !y || (ea && !extra) || (!residual) != (!residual_out))
+    return fail(NVFP4_ERR_NULL, "%s: NULL pointer (residual and residual_out go together)", fn);
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(residual_out, 16) ||
+      !aligned(weight, 16) || !aligned(y, ya) || (ea && !aligned(extra, ea)) ||
+      !aligned(extra_in, 4))
+    return fail(NVFP4_ERR_ALIGN,
+                "%s: x, residual, residual_out and weight must be 16-byte aligned, the output "
+                "%d-byte", fn, (int)ya);
+  const size_t numel = (size_t)M * (size_t)H;
+  const size_t xb = numel * (x_type == NVFP4_F32 ? 4 : 2);
+  const size_t rb = residual ? numel * (residual_type == NVFP4_F32 ? 4 : 2) : 0;
+  const size_t wb = (size_t)H * 2;
+  const void* outs[3] = {y, extra, residual_out};
+  const size_t ob[3] = {yb, eb, rb};
+  for (int i = 0; i < 3; ++i) {
+    if (overlap(outs[i], ob[i], x, xb) || overlap(outs[i], ob[i], weight, wb) ||
+        overlap(outs[i], ob[i], extra_in, 4) ||
+        (outs[i] != residual && overlap(outs[i], ob[i], residual, rb)) ||
+        (i < 2 && outs[i] == residual && overlap(outs[i], ob[i], residual, rb)))
+      return fail(NVFP4_ERR_ALIAS, "%s: an output overlaps an input", fn);
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], ob[i], outs[j], ob[j]))
+        return fail(NVFP4_ERR_ALIAS, "%s: two outputs overlap", fn);
+  }
+  *a = {};
+  a->x = x;
+  a->residual = residual;
+  a->residual_out = residual_out;
+  a->weight = weight;
+  a->M = M;
+  a->H = H;
+  a->eps = eps;
+  a->x_f32 = x_type == NVFP4_F32;
+  a->residual_f32 = residual_type == NVFP4_F32;
+  a->out = const_cast<void*>(y);
+  a->out_scales = const_cast<void*>(extra);
+  return NVFP4_OK;
+}
+
+}  // namespace
+
+nvfp4_status nvfp4_add_rmsnorm(const void* x, int x_type, const void* residual,
+                               void* residual_out, int residual_type, const uint16_t* weight,
+                               float eps, int64_t M, int64_t H, uint16_t* y, hipStream_t stream) {
+  clear_error();
+  nvfp4::NormArgs a;
+  bool nothing;
+  const size_t numel = M > 0 && H > 0 ? (size_t)M * (size_t)H : 0;
+  const nvfp4_status st =
+      norm_checks("nvfp4_add_rmsnorm", x, x_type, residual, residual_out, residual_type, weight,
+                  eps, M, H, 8, y, numel * 2, 16, nullptr, 0, 0, nullptr, &a, &nothing);
+  if (st != NVFP4_OK || nothing) return st;
+  a.form = nvfp4::NormForm::bf16;
+  return hip_result(nvfp4::launch_add_rmsnorm(a, stream), "nvfp4_add_rmsnorm launch");
+}
+
+nvfp4_status nvfp4_add_rmsnorm_e4m3(const void* x, int x_type, const void* residual,
+                                    void* residual_out, int residual_type,
+                                    const uint16_t* weight, float eps, int64_t M, int64_t H,
+                                    int64_t group, uint8_t* y8, float* scales,
+                                    hipStream_t stream) {
+  clear_error();
+  if ((group != 0 && group != 32 && group != 64 && group != 128) ||
+      (group != 0 && H % group != 0))
+    return fail(NVFP4_ERR_SHAPE,
+                "nvfp4_add_rmsnorm_e4m3: group must be 0, 32, 64 or 128 and divide H "
+                "(group=%lld H=%lld)", (long long)group, (long long)H);
+  nvfp4::NormArgs a;
+  bool nothing;
+  const size_t numel = M > 0 && H > 0 ? (size_t)M * (size_t)H : 0;
+  const nvfp4_status st =
+      norm_checks("nvfp4_add_rmsnorm_e4m3", x, x_type, residual, residual_out, residual_type,
+                  weight, eps, M, H, 8, y8, numel, 8, scales,
+                  group ? numel / (size_t)group * 4 : M > 0 ? (size_t)M * 4 : 0, 4, nullptr, &a,
+                  &nothing);
+  if (st != NVFP4_OK || nothing) return st;
+  a.form = nvfp4::NormForm::e4m3;
+  a.group = (int)group;
+  return hip_result(nvfp4::launch_add_rmsnorm(a, stream), "nvfp4_add_rmsnorm_e4m3 launch");
+}
+
+nvfp4_status nvfp4_add_rmsnorm_nvfp4(const void* x, int x_type, const void* residual,
+                                     void* residual_out, int residual_type,
+                                     const uint16_t* weight, float eps, int64_t M, int64_t H,
+                                     const float* gscale, uint8_t* codes, uint8_t* scales,
+                                     hipStream_t stream) {
+  clear_error();
+  nvfp4::NormArgs a;
+  bool nothing;
+  const size_t numel = M > 0 && H > 0 ? (size_t)M * (size_t)H : 0;
+  const nvfp4_status st =
+      norm_checks("nvfp4_add_rmsnorm_nvfp4", x, x_type, residual, residual_out, residual_type,
+                  weight, eps, M, H, 32, codes, numel / 2, 8, scales, numel / 16, 1, gscale, &a,
+                  &nothing);
+  if (st != NVFP4_OK || nothing) return st;
+  if (!gscale) return fail(NVFP4_ERR_NULL, "nvfp4_add_rmsnorm_nvfp4: gscale is NULL");
+  a.form = nvfp4::NormForm::nvfp4;
+  a.gscale = gscale;
+  return hip_result(nvfp4::launch_add_rmsnorm(a, stream), "nvfp4_add_rmsnorm_nvfp4 launch");
+}
+
+namespace {
+
+// Bytes from a cache's first to past its last element (0: none).
+size_t cache_bytes(const nvfp4_kv_cache& c) {
+  if (c.num_blocks == 0) return 0;
+  const int64_t last = (c.num_blocks - 1) * c.stride_block + (c.page - 1) * c.stride_token +
+                       (c.n_kv_heads - 1) * c.stride_head + c.D;
+  return (size_t)last * (c.type == NVFP4_E4M3 ? 1 : 2);
+}
+
+nvfp4_status cache_checks(const char* fn, const nvfp4_kv_cache& c) {
+  if (c.type != NVFP4_BF16 && c.type != NVFP4_E4M3)
+    return fail(NVFP4_ERR_SHAPE, "%s: the cache is bf16 or E4M3 (type %d)", fn, c.type);
+  const int64_t unit = c.type == NVFP4_E4M3 ? 16 : 8;
+  if (c.num_blocks < 0 || c.page < 1 || c.n_kv_heads < 1 || c.D < 1 || c.stride_block < c.D ||
+      c.stride_token < c.D || c.stride_head < c.D || c.stride_block % unit ||
+      c.stride_token % unit || c.stride_head % unit)
+    return fail(NVFP4_ERR_SHAPE,
+                "%s: cache num_blocks=%lld page=%lld heads=%lld D=%lld: need num_blocks >= 0, the "
+                "others >= 1, and strides (%lld, %lld, %lld) >= D, multiples of %lld", fn,
+                (long long)c.num_blocks, (long long)c.page, (long long)c.n_kv_heads,
+                (long long)c.D, (long long)c.stride_block, (long long)c.stride_token,
+                (long long)c.stride_head, (long long)unit);
+  if (c.num_blocks > 0x7FFFFFFF || c.page > (1 << 20) || c.n_kv_heads > NVFP4_MAX_HEADS ||
+      c.D > NVFP4_ROPE_MAX_D || c.stride_token >= (1 << 26) || c.stride_head >= (1LL << 40) ||
+      c.stride_block >= (1LL << 40) || (__int128)c.num_blocks * c.stride_block >= (1LL << 58))
+    return fail(NVFP4_ERR_UNSUPPORTED,
+                "%s: cache num_blocks=%lld page=%lld heads=%lld D=%lld stride_token=%lld is past a "
+                "limit", fn, (long long)c.num_blocks, (long long)c.page, (long long)c.n_kv_heads,
+                (long long)c.D, (long long)c.stride_token);
+  if (c.num_blocks == 0) return NVFP4_OK;
+  if (!c.k || !c.v || c.k == c.v || (c.type == NVFP4_E4M3 && (!c.k_scale || !c.v_scale)))
+    return fail(NVFP4_ERR_NULL, "%s: the cache's k and v (and an E4M3 cache's scales) must be "
+                "non-NULL and differ", fn);
+  if (!aligned(c.k, 16) || !aligned(c.v, 16) ||
+      (c.type == NVFP4_E4M3 && (!aligned(c.k_scale, 4) || !aligned(c.v_scale, 4))))
+    return fail(NVFP4_ERR_ALIGN, "%s: the cache must be 16-byte aligned, its scales 4-byte", fn);
+  return NVFP4_OK;
+}
+
+}  // namespace
+
+nvfp4_status nvfp4_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                               const void* v, int64_t v_stride, int x_type,
+                               const int64_t* positions, const int64_t* slots,
+                               const float* inv_freq, int64_t T, int64_t Hq, int64_t D,
+                               int64_t R, int interleaved, float rope_scale, uint16_t* q_out,
+                               const nvfp4_kv_cache* cache, hipStream_t stream) {
+  clear_error();
+  const char* fn = "nvfp4_rope_append";
+  if (T < 0 || Hq < 0 || D < 16 || D % 16 || R < 0 || R > D || R % 16)
+    return fail(NVFP4_ERR_SHAPE,
+                "%s: need T, Hq >= 0, D >= 16, 0 <= R <= D, D and R multiples of 16 (T=%lld "
+                "Hq=%lld D=%lld R=%lld)", fn, (long long)T, (long long)Hq, (long long)D,
+                (long long)R);
+  if (x_type != NVFP4_BF16 && x_type != NVFP4_F32)
+    return fail(NVFP4_ERR_SHAPE, "%s: q, k and v are bf16 or fp32 (type %d)", fn, x_type);
+  if (interleaved != 0 && interleaved != 1)
+    return fail(NVFP4_ERR_SHAPE, "%s: interleaved is 0 or 1", fn);
+  if (!(rope_scale > -3.0e38f && rope_scale < 3.0e38f))
+    return fail(NVFP4_ERR_SHAPE, "%s: rope_scale must be finite", fn);
+  if (T > NVFP4_MAX_ROWS || Hq > NVFP4_MAX_HEADS || D > NVFP4_ROPE_MAX_D)
+    return fail(NVFP4_ERR_UNSUPPORTED, "%s: T=%lld (max %d), Hq=%lld (max %d), D=%lld (max %d)",
+                fn, (long long)T, NVFP4_MAX_ROWS, (long long)Hq, NVFP4_MAX_HEADS, (long long)D,
+                NVFP4_ROPE_MAX_D);
+  int64_t Hkv = 0;
+  if (cache) {
+    const nvfp4_status st = cache_checks(fn, *cache);
+    if (st != NVFP4_OK) return st;
+    Hkv = cache->n_kv_heads;
+    if (cache->D != D)
+      return fail(NVFP4_ERR_SHAPE, "%s: D=%lld, the cache has %lld", fn, (long long)D,
+                  (long long)cache->D);
+  }
+  const int64_t unit = x_type == NVFP4_F32 ? 4 : 8;
+  if ((Hq && (q_stride < Hq * D || q_stride % unit)) ||
+      (Hkv && (k_stride < Hkv * D || v_stride < Hkv * D || k_stride % unit || v_stride % unit)))
+    return fail(NVFP4_ERR_SHAPE,
+                "%s: token strides (%lld, %lld, %lld) must hold the heads and be multiples of "
+                "%lld", fn, (long long)q_stride, (long long)k_stride, (long long)v_stride,
+                (long long)unit);
+  const int64_t most = 1LL << 36;
+  if (q_stride > most || k_stride > most || v_stride > most)
+    return fail(NVFP4_ERR_UNSUPPORTED, "%s: a token stride is past %lld", fn, (long long)most);
+  if (T == 0 || (Hq == 0 && Hkv == 0)) return NVFP4_OK;
+  if ((Hq && (!q || !q_out)) || (Hkv && (!k || !v || !slots)) || !positions ||
+      (R > 0 && !inv_freq))
+    return fail(NVFP4_ERR_NULL, "%s: NULL pointer", fn);
+  if ((Hq && (!aligned(q, 16) || !aligned(q_out, 16))) ||
+      (Hkv && (!aligned(k, 16) || !aligned(v, 16) || !aligned(slots, 8))) ||
+      !aligned(positions, 8) || !aligned(inv_freq, 4))
+    return fail(NVFP4_ERR_ALIGN,
+                "%s: q, k, v and q_out must be 16-byte, positions and slots 8-byte aligned", fn);
+  const size_t es = x_type == NVFP4_F32 ? 4 : 2;
+  const size_t qb = Hq ? ((size_t)(T - 1) * q_stride + Hq * D) * es : 0;
+  const size_t kb = Hkv ? ((size_t)(T - 1) * k_stride + Hkv * D) * es : 0;
+  const size_t vb = Hkv ? ((size_t)(T - 1) * v_stride + Hkv * D) * es : 0;
+  const size_t ob = (size_t)T * Hq * D * 2, tb = (size_t)T * 8, fb = (size_t)R * 2;
+  const size_t cb = cache ? cache_bytes(*cache) : 0;
+  const void* outs[3] = {Hq ? q_out : nullptr, cache ? cache->k : nullptr,
+                         cache ? cache->v : nullptr};
+  const size_t obytes[3] = {ob, cb, cb};
+  const bool scaled = cache && cache->type == NVFP4_E4M3;
+  for (int i = 0; i < 3; ++i) {
+    const void* o = outs[i];
+    const size_t n = obytes[i];
+    if ((Hq && overlap(o, n, q, qb)) || (Hkv && overlap(o, n, k, kb)) ||
+        (Hkv && overlap(o, n, v, vb)) || overlap(o, n, positions, tb) ||
+        (Hkv && overlap(o, n, slots, tb)) || overlap(o, n, inv_freq, fb) ||
+        (scaled && (overlap(o, n, cache->k_scale, 4) || overlap(o, n, cache->v_scale, 4))))
+      return fail(NVFP4_ERR_ALIAS, "%s: an output overlaps an input", fn);
+    // k and v may lie in each other's gaps; q_out may not lie in theirs
+    if (i > 0 && overlap(o, n, outs[0], ob))
+      return fail(NVFP4_ERR_ALIAS, "%s: q_out overlaps the cache", fn);
+  }
+  nvfp4::RopeArgs a = {};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.positions = positions;
+  a.slots = slots;
+  a.inv_freq = inv_freq;
+  a.T = T;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.R = R;
+  a.rope_scale = rope_scale;
+  a.x_f32 = x_type == NVFP4_F32;
+  a.interleaved = interleaved != 0;
+  a.q_out = q_out;
+  if (cache) {
+    a.cache_e4m3 = scaled;
+    a.k_cache = cache->k;
+    a.v_cache = cache->v;
+    a.num_blocks = cache->num_blocks;
+    a.page = cache->page;
+    a.sb = cache->stride_block;
+    a.st = cache->stride_token;
+    a.sh = cache->stride_head;
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+  } else {
+    a.page = 1;
+  }
+  return hip_result(nvfp4::launch_rope_append(a, stream), "nvfp4_rope_append launch");
+}
+
+namespace {
+
+bool attn_sizes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv, int64_t D) {
+  return B >= 0 && Q >= 0 && Hkv >= 1 && Hq >= 0 && Hq % Hkv == 0 && B <= NVFP4_ATTN_MAX_B &&
+         Q <= NVFP4_ATTN_MAX_Q && Hq <= NVFP4_MAX_HEADS && (D == 64 || D == 128 || D == 256);
+}
+
+}  // namespace
+
+size_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv,
+                                             int64_t D) {
+  if (!attn_sizes(B, Q, Hq, Hkv, D) || Hq == 0) return 0;
+  return nvfp4::attn_workspace_bytes(B, Q, Hq, Hkv, D);
+}
+
+nvfp4_status nvfp4_paged_attention(const uint16_t* q, const nvfp4_kv_cache* cache,
+                                   const int32_t* block_table, const int32_t* seq_lens,
+                                   int64_t B, int64_t Q, int64_t Hq, int64_t max_blocks,
+                                   float scale, int64_t window, uint16_t* out, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream) {
+  clear_error();
+  const char* fn = "nvfp4_paged_attention";
+  if (!cache) return fail(NVFP4_ERR_NULL, "%s: cache is NULL", fn);
+  const nvfp4_status st = cache_checks(fn, *cache);
+  if (st != NVFP4_OK) return st;
+  const int64_t Hkv = cache->n_kv_heads, D = cache->D;
+  if (B < 0 || Q < 0 || Hq < 0 || Hq % Hkv || max_blocks < 0 || window < 0)
+    return fail(NVFP4_ERR_SHAPE,
+                "%s: need B, Q, max_blocks, window >= 0 and Hq a multiple of the cache's heads "
+                "(B=%lld Q=%lld Hq=%lld Hkv=%lld)", fn, (long long)B, (long long)Q,
+                (long long)Hq, (long long)Hkv);
+  if (!attn_sizes(B, Q, Hq, Hkv, D))
+    return fail(NVFP4_ERR_UNSUPPORTED,
+                "%s: B=%lld (max %d), Q=%lld (max %d), Hq=%lld (max %d), D=%lld (64, 128 or 256)",
+                fn, (long long)B, NVFP4_ATTN_MAX_B, (long long)Q, NVFP4_ATTN_MAX_Q,
+                (long long)Hq, NVFP4_MAX_HEADS, (long long)D);
+  if (max_blocks > 0x7FFFFFFF || window > 0x7FFFFFFF)
+    return fail(NVFP4_ERR_UNSUPPORTED, "%s: max_blocks=%lld or window=%lld is past 2^31 - 1", fn,
+                (long long)max_blocks, (long long)window);
+  if (B == 0 || Q == 0 || Hq == 0) return NVFP4_OK;
+  nvfp4::AttnArgs a = {};
+  a.k_cache = cache->k;
+  a.v_cache = cache->v;
+  a.num_blocks = cache->num_blocks;
+  a.page = cache->page;
+  a.sb = cache->stride_block;
+  a.st = cache->stride_token;
+  a.sh = cache->stride_head;
+  a.cache_e4m3 = cache->type == NVFP4_E4M3;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.B = B;
+  a.Q = Q;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.D = D;
+  a.max_blocks = max_blocks;
+  a.window = window;
+  if (!nvfp4::attn_fits(a))
+    return fail(NVFP4_ERR_UNSUPPORTED,
+                "%s: B * heads * max_blocks * page has more than 2^31 steps of keys", fn);
+  if (!q || !seq_lens || !out || (max_blocks && !block_table))
+    return fail(NVFP4_ERR_NULL, "%s: NULL pointer", fn);
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
+    return fail(NVFP4_ERR_ALIGN,
+                "%s: q and out must be 16-byte, block_table and seq_lens 4-byte aligned", fn);
+  const size_t need = nvfp4::attn_workspace_bytes(B, Q, Hq, Hkv, D);
+  if (!workspace || workspace_bytes < need)
+    return fail(NVFP4_ERR_WORKSPACE, "%s: the workspace needs %zu bytes, %zu given", fn, need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (!aligned(workspace, 256))
+    return fail(NVFP4_ERR_ALIGN, "%s: the workspace must be 256-byte aligned", fn);
+  const size_t qb = (size_t)B * Q * Hq * D * 2, cb = cache_bytes(*cache);
+  const size_t tb = (size_t)B * max_blocks * 4, lb = (size_t)B * 4;
+  const void* outs[2] = {out, workspace};
+  const size_t ob[2] = {qb, need};
+  for (int i = 0; i < 2; ++i)
+    if (overlap(outs[i], ob[i], q, qb) || overlap(outs[i], ob[i], cache->k, cb) ||
+        overlap(outs[i], ob[i], cache->v, cb) || overlap(outs[i], ob[i], block_table, tb) ||
+        overlap(outs[i], ob[i], seq_lens, lb) ||
+        (cache->type == NVFP4_E4M3 && (overlap(outs[i], ob[i], cache->k_scale, 4) ||
+                                       overlap(outs[i], ob[i], cache->v_scale, 4))))
+      return fail(NVFP4_ERR_ALIAS, "%s: the output or the workspace overlaps an input", fn);
+  if (overlap(out, qb, workspace, need))
+    return fail(NVFP4_ERR_ALIAS, "%s: the output and the workspace overlap", fn);
+  a.q = q;
+  a.table = block_table;
+  a.lens = seq_lens;
+  a.scale = scale;
+  a.out = out;
+  a.workspace = workspace;
+  return hip_result(nvfp4::launch_paged_attention(a, stream), "nvfp4_paged_attention launch");
+}
+
+namespace {
+
+bool verify_sizes(int64_t B, int64_t V) {
+  return B >= 0 && V >= 1 && B <= NVFP4_VERIFY_MAX_B && V <= NVFP4_VERIFY_MAX_V;
+}
+
+}  // namespace
+
+size_t nvfp4_verify_draft_workspace_bytes(int64_t B, int64_t V) {
+  return verify_sizes(B, V) ? nvfp4::verify_workspace_bytes(B, V) : 0;
+}
+
+nvfp4_status nvfp4_verify_draft(const float* target_p, const float* draft_p, const int32_t* draft,
+                                const int32_t* n_draft, const float* u_accept,
+                                const float* u_sample, int64_t B, int64_t Q, int64_t V,
+                                int32_t* tokens, int32_t* n_accepted, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
+  clear_error();
+  const char* fn = "nvfp4_verify_draft";
+  if (B < 0 || Q < 0 || V < 1)
+    return fail(NVFP4_ERR_SHAPE, "%s: need B, Q >= 0 and V >= 1 (B=%lld Q=%lld V=%lld)", fn,
+                (long long)B, (long long)Q, (long long)V);
+  if (!verify_sizes(B, V) || Q > NVFP4_VERIFY_MAX_Q)
+    return fail(NVFP4_ERR_UNSUPPORTED, "%s: B=%lld (max %d), Q=%lld (max %d), V=%lld (max %d)",
+                fn, (long long)B, NVFP4_VERIFY_MAX_B, (long long)Q, NVFP4_VERIFY_MAX_Q,
+                (long long)V, NVFP4_VERIFY_MAX_V);
+  if (B == 0) return NVFP4_OK;
+  if (!target_p || !u_sample || !tokens || !n_accepted || (Q && (!draft || !u_accept)))
+    return fail(NVFP4_ERR_NULL, "%s: NULL pointer", fn);
+  if (!aligned(target_p, 4) || !aligned(draft_p, 4) || !aligned(draft, 4) ||
+      !aligned(n_draft, 4) || !aligned(u_accept, 4) || !aligned(u_sample, 4) ||
+      !aligned(tokens, 4) || !aligned(n_accepted, 4))
+    return fail(NVFP4_ERR_ALIGN, "%s: every pointer must be 4-byte aligned", fn);
+  const size_t need = nvfp4::verify_workspace_bytes(B, V);
+  if (!workspace || workspace_bytes < need)
+    return fail(NVFP4_ERR_WORKSPACE, "%s: the workspace needs %zu bytes, %zu given", fn, need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (!aligned(workspace, 256))
+    return fail(NVFP4_ERR_ALIGN, "%s: the workspace must be 256-byte aligned", fn);
+  const size_t pb = (size_t)B * (Q + 1) * V * 4, qb = (size_t)B * Q * V * 4;
+  const size_t db = (size_t)B * Q * 4, bb = (size_t)B * 4;
+  const void* outs[3] = {tokens, n_accepted, workspace};
+  const size_t ob[3] = {(size_t)B * (Q + 1) * 4, bb, need};
+  for (int i = 0; i < 3; ++i) {
+    if (overlap(outs[i], ob[i], target_p, pb) || overlap(outs[i], ob[i], draft_p, qb) ||
+        overlap(outs[i], ob[i], draft, db) || overlap(outs[i], ob[i], n_draft, bb) ||
+        overlap(outs[i], ob[i], u_accept, db) || overlap(outs[i], ob[i], u_sample, bb))
+      return fail(NVFP4_ERR_ALIAS, "%s: an output or the workspace overlaps an input", fn);
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], ob[i], outs[j], ob[j]))
+        return fail(NVFP4_ERR_ALIAS, "%s: two outputs overlap", fn);
+  }
+  nvfp4::VerifyArgs a = {};
+  a.p = target_p;
+  a.q = Q ? draft_p : nullptr;
+  a.draft = draft;
+  a.n_draft = n_draft;
+  a.u_accept = u_accept;
+  a.u_sample = u_sample;
+  a.B = B;
+  a.Q = Q;
+  a.V = V;
+  a.tokens = tokens;
+  a.accepted = n_accepted;
+  a.workspace = workspace;
+  return hip_result(nvfp4::launch_verify_draft(a, stream), "nvfp4_verify_draft launch");
+}
+
 nvfp4_status nvfp4_stream_read(const void* buf, size_t bytes, uint32_t* sink,
                                hipStream_t stream) {
   clear_error();

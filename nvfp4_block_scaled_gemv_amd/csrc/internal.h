@@ -152,4 +152,75 @@ hipError_t launch_moe(const uint8_t* w13_codes, const uint8_t* w13_scales,
                       int64_t I, int topk, const MoeShared* shared, const MoeW4a4* w4a4,
                       float* y, void* workspace, hipStream_t stream);
 
+// RMS norm with the residual's addition (norm.hip). H % 8 == 0 (nvfp4: % 32),
+// H <= NVFP4_NORM_MAX_H, H % group == 0; residual NULL: none. residual_out may
+// be residual itself.
+enum class NormForm { bf16, e4m3, nvfp4 };
+struct NormArgs {
+  const void* x;          // [M, H] bf16 or fp32 (x_f32)
+  const void* residual;   // [M, H] bf16 or fp32 (residual_f32), or NULL
+  void* residual_out;
+  const uint16_t* weight; // bf16 [H]
+  int64_t M, H;
+  float eps;
+  bool x_f32, residual_f32;
+  NormForm form;
+  int group;              // e4m3: elements per scale, 0 for a whole row
+  const float* gscale;    // nvfp4: the static tensor scale
+  void* out;              // bf16 [M, H], E4M3 [M, H] or codes [M, H/2]
+  void* out_scales;       // fp32 [M, H / group] or E4M3 [M, H/16]
+};
+hipError_t launch_add_rmsnorm(const NormArgs& a, hipStream_t stream);
+
+// Rotary positions and the append to a paged cache (rope.hip).
+struct RopeArgs {
+  const void *q, *k, *v;             // [T, heads, D] bf16 or fp32 (x_f32)
+  int64_t q_stride, k_stride, v_stride;   // elements between tokens
+  const int64_t *positions, *slots;  // [T]
+  const float* inv_freq;             // [R / 2]
+  int64_t T, Hq, Hkv, D, R;
+  float rope_scale;
+  bool x_f32, interleaved, cache_e4m3;
+  uint16_t* q_out;                   // bf16 [T, Hq, D]
+  void *k_cache, *v_cache;           // [num_blocks, page, Hkv, D], strided
+  int64_t num_blocks, page, sb, st, sh;   // strides in elements: block, token, head
+  const float *k_scale, *v_scale;    // E4M3 cache: float [1] each
+};
+hipError_t launch_rope_append(const RopeArgs& a, hipStream_t stream);
+
+// Attention of Q new tokens per sequence over a paged cache (paged_attn.hip).
+struct AttnArgs {
+  const uint16_t* q;                 // bf16 [B * Q, Hq, D]
+  const void *k_cache, *v_cache;     // [num_blocks, page, Hkv, D], strided
+  int64_t num_blocks, page, sb, st, sh;
+  const int32_t* table;              // [B, max_blocks]
+  const int32_t* lens;               // [B]
+  int64_t B, Q, Hq, Hkv, D, max_blocks, window;
+  float scale;
+  bool cache_e4m3;
+  const float *k_scale, *v_scale;    // E4M3 cache: float [1] each
+  uint16_t* out;                     // bf16 [B * Q, Hq, D]
+  void* workspace;
+};
+// its steps can be numbered in 31 bits
+bool attn_fits(const AttnArgs& a);
+size_t attn_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv, int64_t D);
+hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream);
+
+// Verification of drafted tokens (verify.hip).
+struct VerifyArgs {
+  const float* p;          // [B, Q + 1, V]
+  const float* q;          // [B, Q, V] or NULL
+  const int32_t* draft;    // [B, Q]
+  const int32_t* n_draft;  // [B] or NULL
+  const float* u_accept;   // [B, Q]
+  const float* u_sample;   // [B]
+  int64_t B, Q, V;
+  int32_t* tokens;         // [B, Q + 1]
+  int32_t* accepted;       // [B]
+  void* workspace;
+};
+size_t verify_workspace_bytes(int64_t B, int64_t V);
+hipError_t launch_verify_draft(const VerifyArgs& a, hipStream_t stream);
+
 }  // namespace nvfp4
