@@ -719,7 +719,7 @@ nvfp4_status nvfp4_paged_attention(const uint16_t* q, const nvfp4_kv_cache* cach
   a.window = window;
   if (!nvfp4::attn_fits(a))
     return fail(NVFP4_ERR_UNSUPPORTED,
-                "%s: B * heads * max_blocks * page has more than 2^31 steps of keys", fn);
+                "%s: B * max_blocks * page has more than 2^31 tiles of 32 keys", fn);
   if (!q || !seq_lens || !out || (max_blocks && !block_table))
     return fail(NVFP4_ERR_NULL, "%s: NULL pointer", fn);
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
