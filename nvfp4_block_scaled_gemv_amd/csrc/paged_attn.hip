@@ -30,8 +30,6 @@
 // at most two per wavefront, that k_attn_join adds in a fixed order. No
 // atomics. Where the table's rows are short (kWholeKeys), one workgroup of
 // eight wavefronts takes a sequence and head whole and joins them in LDS.
-#include <type_traits>
-
 #include "elems.h"
 #include "internal.h"
 
@@ -49,11 +47,18 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;
 // A run has at least this many tiles: fewer records to join.
 constexpr int kMinTiles = 1;
+// s_waitcnt vmcnt(0), no other counter.
+constexpr int kVmcnt0 = 0x0F70;
+// Runs of one head at most.
+constexpr int kMaxRuns = kCus * 4 * 2;
 
-// Keys per tile: 16 KB of K and V at a time.
-constexpr int tile_keys(int D, bool FP8) { return D * (FP8 ? 1 : 2) >= 256 ? 32 : 64; }
-// Wavefronts per SIMD of the split form.
-constexpr int waves_per_simd(int RT, int D) { return 1; }
+constexpr int TK = 32;   // keys per tile
+// Wavefronts per SIMD of the split form. Few long streams read memory best:
+// heads of 256 bytes and more keep 16 KB and more in flight per wavefront with
+// one; smaller heads need two.
+constexpr int waves_per_simd(int RT, int D, bool FP8) {
+  return RT == 1 && D * (FP8 ? 1 : 2) < 256 ? 2 : 1;
+}
 
 struct AttnShape {
   int rows;        // G * Q
@@ -69,11 +74,10 @@ struct AttnShape {
 
 typedef const __attribute__((address_space(4))) int32_t* const_i32;
 
-// The tiles (of TK keys) of one sequence: keys base .. len - 1.
+// The tiles of one sequence: keys base .. len - 1.
 struct Span {
-  int len, base, n;   // n >= 1: an empty sequence has one tile that writes zeros
+  int len, base, n;   // n >= 1: an empty sequence has one tile, of which nobody sees a key
 };
-template <int TK>
 __device__ __forceinline__ Span span_of(const AttnArgs& a, const AttnShape& sh, int len) {
   Span s;
   s.len = len < 0 ? 0 : len > sh.cap ? sh.cap : len;
@@ -83,45 +87,70 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const AttnShape& sh, 
   return s;
 }
 
-__device__ __forceinline__ int wave_sum_i32(int v) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
-  return __builtin_amdgcn_readfirstlane(v);
+// Inclusive sums over the 64 lanes, by DPP: within rows of 16, then from each
+// row's last lane to the rows after it.
+__device__ __forceinline__ int scan64(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, true);   // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, true);   // row_bcast:31
+  return v;
 }
 
-// Tiles of all sequences, by every wavefront for itself.
-template <int TK>
-__device__ __forceinline__ int total_tiles(const AttnArgs& a, const AttnShape& sh) {
-  const int lane = threadIdx.x & 63, B = (int)a.B;
-  int t = 0;
-  for (int b = lane; b < B; b += 64) t += span_of<TK>(a, sh, a.lens[b]).n;
-  return wave_sum_i32(t);
-}
-// The sequence that holds tile u, and the tiles before it.
-template <int TK>
-__device__ __forceinline__ int find_sequence(const AttnArgs& a, const AttnShape& sh, int u,
-                                             int& before) {
-  const int lane = threadIdx.x & 63, B = (int)a.B;
-  int run = 0;
-  for (int b0 = 0; b0 < B; b0 += 64) {
-    const int n = b0 + lane < B ? span_of<TK>(a, sh, a.lens[b0 + lane]).n : 0;
-    int incl = n;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(incl, off, 64);
-      if (lane >= off) incl += o;
+// The tiles of all sequences, by every wavefront for itself (all 64 lanes).
+struct Tiles {
+  const AttnArgs& a;
+  const AttnShape& sh;
+  const int lane;
+  int len, n, incl;   // of sequence `lane`, and the tiles up to it (of the first 64)
+  int total;
+  __device__ __forceinline__ Tiles(const AttnArgs& a_, const AttnShape& sh_)
+      : a(a_), sh(sh_), lane(threadIdx.x & 63) {
+    len = lane < (int)a.B ? a.lens[lane] : 0;
+    n = lane < (int)a.B ? span_of(a, sh, len).n : 0;
+    incl = scan64(n);
+    total = __builtin_amdgcn_readlane(incl, 63);
+    for (int b0 = 64; b0 < (int)a.B; b0 += 64) {
+      const int b = b0 + lane;
+      const int m = b < (int)a.B ? span_of(a, sh, a.lens[b]).n : 0;
+      total += __builtin_amdgcn_readlane(scan64(m), 63);
     }
-    const uint64_t past = __ballot(run + incl > u);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      before = run + __builtin_amdgcn_readlane(incl - n, l);
-      return b0 + l;
-    }
-    run += __builtin_amdgcn_readlane(incl, 63);
   }
-  before = 0;
-  return 0;   // not reached for u below the total
-}
+  // The sequence that holds tile u, its length, and the tiles before it.
+  __device__ __forceinline__ int find(int u, int& before, int& its_len) const {
+    int run = 0, len_l = len, n_l = n, incl_l = incl;
+    for (int b0 = 0;;) {
+      const uint64_t past = __ballot(run + incl_l > u);
+      if (past) {
+        const int l = __builtin_ctzll(past);
+        before = run + __builtin_amdgcn_readlane(incl_l - n_l, l);
+        its_len = __builtin_amdgcn_readlane(len_l, l);
+        return b0 + l;
+      }
+      run += __builtin_amdgcn_readlane(incl_l, 63);
+      b0 += 64;
+      if (b0 >= (int)a.B) break;   // not reached for u below the total
+      len_l = b0 + lane < (int)a.B ? a.lens[b0 + lane] : 0;
+      n_l = b0 + lane < (int)a.B ? span_of(a, sh, len_l).n : 0;
+      incl_l = scan64(n_l);
+    }
+    before = its_len = 0;
+    return 0;
+  }
+  // The tiles before sequence b.
+  __device__ __forceinline__ int before(int b) const {
+    int run = 0, n_l = n, incl_l = incl;
+    for (int b0 = 0; b - b0 >= 64;) {
+      run += __builtin_amdgcn_readlane(incl_l, 63);
+      b0 += 64;
+      n_l = b0 + lane < (int)a.B ? span_of(a, sh, a.lens[b0 + lane]).n : 0;
+      incl_l = scan64(n_l);
+    }
+    return run + __builtin_amdgcn_readlane(incl_l - n_l, b & 63);
+  }
+};
 // Run w starts at tile start(w); the first r runs have q + 1 tiles and the
 // others q (total = nw * q + r). of(s): the run that has tile s.
 struct Runs {
@@ -176,6 +205,20 @@ struct VRow {
       }
     }
   }
+  // some element is infinite or NaN (E4M3: NaN): a half, or byte, with all
+  // exponent bits (and E4M3's mantissa) set
+  __device__ __forceinline__ bool not_finite() const {
+    constexpr uint32_t kSet = FP8 ? 0x7F7F7F7Fu : 0x7F807F80u;
+    constexpr uint32_t kOnes = FP8 ? 0x01010101u : 0x00010001u;
+    constexpr uint32_t kTops = FP8 ? 0x80808080u : 0x80008000u;
+    uint32_t hit = 0u;
+#pragma unroll
+    for (int d = 0; d < kDw; ++d) {
+      const uint32_t x = (w[d] & kSet) ^ kSet;   // a field of zeros
+      hit |= (x - kOnes) & ~x & kTops;
+    }
+    return hit != 0u;
+  }
   __device__ __forceinline__ uint32_t get(int d) const {   // dims 2 d, 2 d + 1
     if constexpr (FP8)
       return (d & 1) ? e4m3x2_to_bf16<1>(w[d >> 1]) : e4m3x2_to_bf16<0>(w[d >> 1]);
@@ -184,9 +227,15 @@ struct VRow {
   }
 };
 
-// The state of one wavefront over the keys of one sequence and head, and its
-// passes over tiles.
-template <int D, bool FP8, int RT, bool PG, int TK>
+// A tile of a wavefront's run.
+struct Cursor {
+  int b, len;   // its sequence
+  int key;      // its first key
+  int left;     // tiles of the sequence from it on
+};
+
+// One wavefront's pass over tiles of one head.
+template <int D, bool FP8, int RT, bool PG>
 struct AttnWave {
   static constexpr int NU = TK / 16;           // runs of 16 keys
   static constexpr int NP = TK / 32;           // products over the keys
@@ -194,17 +243,18 @@ struct AttnWave {
   static constexpr int NV = D / 16;            // dims per lane of V
   static constexpr int ES = FP8 ? 1 : 2;
   static constexpr int KL = D * ES / 64;       // 16-byte loads of K per lane and 16 keys
-  static constexpr uint64_t kAll = TK == 64 ? ~0ull : (1ull << (TK & 63)) - 1;
+  static constexpr int NO = PG ? NU : 1;
+  static constexpr uint32_t kAll = 0xFFFFFFFFu;
 
   const AttnArgs& a;
   const AttnShape& sh;
   const int lane, n, g;
-  const int b, Q, G, row0, rows;
-  const Span sp;
+  const int h, Q, G, row0, rows;
   const float c;                               // scale of the scores, log2
   const int64_t head_off;
   const uint32_t stb, k_lane, v_dim, v_lane;
-  const const_i32 table;
+  const const_i32 lens;
+  int len_after;                               // of the sequence after the last cursor's
   bf16x8_t qf[RT][NJ];
   int tok[RT];
   f32x4_t O[RT][NV];
@@ -215,37 +265,59 @@ struct AttnWave {
   // resolve(), which turns them into offsets: PG, runs of 16 keys inside one
   // page each (uniform); otherwise one offset per lane, for key lane % TK. ok:
   // bit per key, its page exists (page 0 is read in its place).
-  int ids[PG ? NU : 1], in_page[PG ? NU : 1];
-  int64_t off[PG ? NU : 1];
-  uint64_t ok;
+  int ids[NO], in_page[NO];
+  int64_t off[NO];
+  uint32_t ok;
 
-  __device__ __forceinline__ AttnWave(const AttnArgs& a_, const AttnShape& sh_, int b_, int h,
-                                      int row0_, const Span& sp_, float c_)
-      : a(a_), sh(sh_), lane(threadIdx.x & 63), n(lane & 15), g(lane >> 4), b(b_), Q((int)a_.Q),
+  __device__ __forceinline__ AttnWave(const AttnArgs& a_, const AttnShape& sh_, int h_, int row0_,
+                                      float c_)
+      : a(a_), sh(sh_), lane(threadIdx.x & 63), n(lane & 15), g(lane >> 4), h(h_), Q((int)a_.Q),
         G(sh_.G), row0(row0_), rows(sh_.rows - row0_ < RT * 16 ? sh_.rows - row0_ : RT * 16),
-        sp(sp_), c(c_), head_off((int64_t)h * a_.sh), stb((uint32_t)a_.st * ES),
+        c(c_), head_off((int64_t)h_ * a_.sh), stb((uint32_t)a_.st * ES),
         k_lane((uint32_t)n * stb + (uint32_t)g * 16),
         v_dim((uint32_t)n * (NV > 8 ? 8 : NV) * ES), v_lane((uint32_t)(g * 4) * stb + v_dim),
-        table((const_i32)(uintptr_t)(a_.table + (int64_t)b_ * a_.max_blocks)) {
+        lens((const_i32)(uintptr_t)a_.lens) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int r = row0 + rt * 16 + n;
-      const bool live = r < sh.rows;
-      tok[rt] = live ? r / G : -1;
-      const uint16_t* qp = a.q + ((int64_t)(b * (int64_t)Q + (live ? tok[rt] : 0)) * a.Hq + h * G +
-                                  (live ? r - tok[rt] * G : 0)) * D;
+      tok[rt] = r < sh.rows ? r / G : -1;
+    }
+    clear();
+  }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int d0 = FP8 ? (j >> 1) * 64 + g * 16 + (j & 1) * 8 : j * 32 + g * 8;
-        u32x4_t v = *reinterpret_cast<const u32x4_t*>(qp + d0);
-        if (!live) v = u32x4_t{0, 0, 0, 0};
-        qf[rt][j] = __builtin_bit_cast(bf16x8_t, v);
-      }
+    for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
       for (int t = 0; t < NV; ++t) O[rt][t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
       m[rt] = -INFINITY;
       l[rt] = 0.0f;
     }
+  }
+  __device__ __forceinline__ void load_q(int b) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int r = row0 + rt * 16 + n;
+      const bool live = tok[rt] >= 0;
+      const uint16_t* qp = a.q + ((int64_t)(b * (int64_t)Q + (live ? tok[rt] : 0)) * a.Hq + h * G +
+                                  (live ? r - tok[rt] * G : 0)) * D;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int d0 = FP8 ? (j >> 1) * 64 + g * 16 + (j & 1) * 8 : j * 32 + g * 8;
+        // rows that do not exist read another's: nothing of them is written
+        qf[rt][j] = *reinterpret_cast<const bf16x8_t*>(qp + d0);
+      }
+    }
+  }
+  __device__ __forceinline__ Cursor first_of(int b, int len, int idx) {
+    const Span s = span_of(a, sh, len);
+    len_after = lens[b + 1 < (int)a.B ? b + 1 : b];
+    return Cursor{b, s.len, s.base + idx * TK, s.n - idx};
+  }
+  // The tile `step` further in c's sequence, or the next one's first (past the
+  // last sequence: any tile, it is not computed).
+  __device__ __forceinline__ Cursor after(const Cursor& c, int step) {
+    if (c.left <= step && c.b + 1 < (int)a.B) return first_of(c.b + 1, len_after, 0);
+    return Cursor{c.b, c.len, c.key + step * TK, c.left - step};
   }
 
   __device__ __forceinline__ int page_of(int key, int& in) const {
@@ -253,49 +325,58 @@ struct AttnWave {
     in = key - pi * (int)a.page;
     return pi < (int)a.max_blocks ? pi : (int)a.max_blocks - 1;
   }
-  __device__ __forceinline__ void fetch(int key0) {
+  // Only for tiles that hold a key: an empty sequence's table has no row.
+  __device__ __forceinline__ void fetch(const Cursor& c) {
     if constexpr (PG) {
+      const const_i32 table = (const_i32)(uintptr_t)(a.table + (int64_t)c.b * a.max_blocks);
 #pragma unroll
-      for (int u = 0; u < NU; ++u) ids[u] = table[page_of(key0 + 16 * u, in_page[u])];
+      for (int u = 0; u < NU; ++u) ids[u] = table[page_of(c.key + 16 * u, in_page[u])];
     } else {
-      const int pi = page_of(key0 + (lane & (TK - 1)), in_page[0]);
-      ids[0] = a.table[(int64_t)b * a.max_blocks + pi];
+      const int pi = page_of(c.key + (lane & (TK - 1)), in_page[0]);
+      ids[0] = a.table[(int64_t)c.b * a.max_blocks + pi];
     }
   }
   __device__ __forceinline__ void resolve() {
     ok = 0;
 #pragma unroll
-    for (int u = 0; u < (PG ? NU : 1); ++u) {
+    for (int u = 0; u < NO; ++u) {
       const bool fine = (uint32_t)ids[u] < (uint32_t)a.num_blocks;
       off[u] = (int64_t)(fine ? ids[u] : 0) * a.sb + (int64_t)in_page[u] * a.st + head_off;
       if (PG)
-        ok |= fine ? 0xFFFFull << (16 * u) : 0ull;
+        ok |= fine ? 0xFFFFu << (16 * u) : 0u;
       else
-        ok = __ballot(fine) & kAll;
+        ok = (uint32_t)__ballot(fine);
     }
   }
-  __device__ __forceinline__ int64_t at_key(int src) const {   // byte offset of lane src's key
+  // byte offset of lane src's key
+  __device__ __forceinline__ int64_t at_key(const int64_t (&off)[NO], int src) const {
     const int lo = __shfl((int)off[0], src, 64);
     const int hi = __shfl((int)(off[0] >> 32), src, 64);
     return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo) * ES;
   }
   // lane's key of V, and of S^T and P: i-th of the tile (of TK / 4)
   __device__ __forceinline__ int key_of(int i) const { return (i >> 2) * 16 + g * 4 + (i & 3); }
-  __device__ __forceinline__ void load_k() {
+  // want: false where no tile follows. The loads are issued all the same, all
+  // lanes from one address: a branch around them would make the waits on both
+  // sides drain everything in flight.
+  __device__ __forceinline__ void load_k(bool want) {
     const uint8_t* const kc = (const uint8_t*)a.k_cache;
+    const uint32_t lane_off = want ? k_lane : 0u;
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const uint8_t* p = PG ? kc + off[PG ? u : 0] * ES + k_lane : kc + at_key(16 * u + n) + g * 16;
+      const uint8_t* p = PG ? kc + off[PG ? u : 0] * ES + lane_off
+                            : want ? kc + at_key(off, 16 * u + n) + g * 16 : kc;
 #pragma unroll
       for (int j = 0; j < KL; ++j) kr[u][j] = load_stream(p + j * 64);
     }
   }
-  __device__ __forceinline__ void load_v() {
+  __device__ __forceinline__ void load_v(bool want) {
     const uint8_t* const vc = (const uint8_t*)a.v_cache;
+    const uint32_t lane_off = want ? v_lane : 0u, st = want ? stb : 0u;
 #pragma unroll
     for (int i = 0; i < TK / 4; ++i)
-      vr[i].load(PG ? vc + off[PG ? i >> 2 : 0] * ES + (uint32_t)(i & 3) * stb + v_lane
-                    : vc + at_key(key_of(i)) + v_dim);
+      vr[i].load(PG ? vc + off[PG ? i >> 2 : 0] * ES + (uint32_t)(i & 3) * st + lane_off
+                    : want ? vc + at_key(off, key_of(i)) + v_dim : vc);
   }
 
   // S^T of the loaded tile, scaled
@@ -324,7 +405,7 @@ struct AttnWave {
     }
   }
   // The running maximum and sum, and P as bf16 pairs.
-  __device__ __forceinline__ void softmax(const f32x4_t (&S)[RT][NU], uint32_t (&pf)[RT][2 * NU]) {
+  __device__ __forceinline__ void softmax(const f32x4_t (&S)[RT][NU], u32x4_t (&pf)[RT][NP]) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       float mx = -INFINITY;
@@ -346,103 +427,16 @@ struct AttnWave {
         const float p0 = __builtin_amdgcn_exp2f(S[rt][e >> 1][(e & 1) * 2] - m_use);
         const float p1 = __builtin_amdgcn_exp2f(S[rt][e >> 1][(e & 1) * 2 + 1] - m_use);
         l[rt] += p0 + p1;
-        pf[rt][e] = pack_bf16(p0, p1);
+        pf[rt][e >> 2][e & 3] = pack_bf16(p0, p1);
       }
     }
   }
-  __device__ __forceinline__ f32x4_t product(u32x4_t v, const uint32_t* pf, f32x4_t acc) const {
-    const u32x4_t pv = {pf[0], pf[1], pf[2], pf[3]};
+  __device__ __forceinline__ f32x4_t product(u32x4_t v, u32x4_t pf, f32x4_t acc) const {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, v),
-                                                   __builtin_bit_cast(bf16x8_t, pv), acc, 0, 0, 0);
+                                                   __builtin_bit_cast(bf16x8_t, pf), acc, 0, 0, 0);
   }
-  // Keys of pages that do not exist: no weight, and no value.
-  __device__ __forceinline__ void hide(uint64_t ok_now, f32x4_t (&S)[RT][NU]) {
-#pragma unroll
-    for (int i = 0; i < TK / 4; ++i) {
-      const bool there = (ok_now >> key_of(i)) & 1u;
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-        S[rt][i >> 2][i & 3] = there ? S[rt][i >> 2][i & 3] : -INFINITY;
-#pragma unroll
-      for (int d = 0; d < VRow<NV, FP8>::kDw; ++d) vr[i].w[d] = there ? vr[i].w[d] : 0u;
-    }
-  }
-
-  // A tile that some row sees only in part.
-  __device__ __forceinline__ void masked_tile(int key0) {
-    fetch(key0);
-    resolve();
-    load_k();
-    load_v();
-    f32x4_t S[RT][NU];
-    uint32_t pf[RT][2 * NU];
-    scores(S);
-    if (ok != kAll) hide(ok, S);
-    const int pos0 = sp.len - Q;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const int hi = tok[rt] < 0 ? -1 : pos0 + tok[rt];
-      const int64_t lo = a.window ? (int64_t)hi - a.window + 1 : 0;
-#pragma unroll
-      for (int e = 0; e < 4 * NU; ++e) {
-        const int key = key0 + key_of(e);
-        if (key > hi || key < lo) S[rt][e >> 2][e & 3] = -INFINITY;
-      }
-    }
-    softmax(S, pf);
-    // A value that no row sees, or that another token sees, may be anything
-    // (0 * inf would reach every row): one product per token, on the values
-    // that it sees, kept by that token's rows.
-    const int t0 = row0 / G, t1 = (row0 + rows - 1) / G;
-    for (int i0 = t0; i0 <= t1; ++i0) {
-      const int hi_key = pos0 + i0;
-      const int64_t lo_key = a.window ? (int64_t)hi_key - a.window + 1 : 0;
-#pragma unroll
-      for (int d = 0; d < NV / 2; ++d) {
-#pragma unroll
-        for (int q = 0; q < NP; ++q) {
-          uint32_t x[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int key = key0 + key_of(q * 8 + i);
-            x[i] = key <= hi_key && key >= lo_key ? vr[q * 8 + i].get(d) : 0u;
-          }
-          const u32x4_t lo = {perm_lo(x[0], x[1]), perm_lo(x[2], x[3]), perm_lo(x[4], x[5]),
-                              perm_lo(x[6], x[7])};
-          const u32x4_t hi = {perm_hi(x[0], x[1]), perm_hi(x[2], x[3]), perm_hi(x[4], x[5]),
-                              perm_hi(x[6], x[7])};
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            const f32x4_t o0 = product(lo, &pf[rt][4 * q], O[rt][2 * d]);
-            const f32x4_t o1 = product(hi, &pf[rt][4 * q], O[rt][2 * d + 1]);
-            const bool mine = tok[rt] == i0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              O[rt][2 * d][i] = mine ? o0[i] : O[rt][2 * d][i];
-              O[rt][2 * d + 1][i] = mine ? o1[i] : O[rt][2 * d + 1][i];
-            }
-          }
-        }
-      }
-    }
-  }
-  // A tile that every row sees, loaded already. MORE: the one `ahead` keys on
-  // is loaded meanwhile (K while the values are multiplied, V while the next
-  // scores are). MORE is a constant, so that the loads in flight are the same
-  // on every path to a wait: a branch around them would drain them all.
-  template <bool MORE>
-  __device__ __forceinline__ void full_tile(int key0, int ahead) {
-    f32x4_t S[RT][NU];
-    uint32_t pf[RT][2 * NU];
-    scores(S);
-    const uint64_t ok_now = ok;
-    if (MORE) {
-      resolve();
-      load_k();
-      fetch(key0 + 2 * ahead);
-    }
-    if (ok_now != kAll) hide(ok_now, S);
-    softmax(S, pf);
+  // O += V^T P^T
+  __device__ __forceinline__ void values(const u32x4_t (&pf)[RT][NP]) {
 #pragma unroll
     for (int d = 0; d < NV / 2; ++d) {
 #pragma unroll
@@ -456,54 +450,126 @@ struct AttnWave {
                             perm_hi(x[6], x[7])};
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          O[rt][2 * d] = product(lo, &pf[rt][4 * q], O[rt][2 * d]);
-          O[rt][2 * d + 1] = product(hi, &pf[rt][4 * q], O[rt][2 * d + 1]);
+          O[rt][2 * d] = product(lo, pf[rt][q], O[rt][2 * d]);
+          O[rt][2 * d + 1] = product(hi, pf[rt][q], O[rt][2 * d + 1]);
         }
       }
     }
-    if (MORE) load_v();
   }
 
-  // The tiles at key0, key0 + stride, .. below key_end. Those that some row
-  // sees only in part lie before full_lo and past full_hi.
-  __device__ __forceinline__ void pass(int key0, int key_end, int stride) {
-    const int64_t full_lo = a.window ? (int64_t)sp.len - a.window : 0;
-    const int full_hi = sp.len - Q;
-    const int full_end = full_hi + 1 - TK < key_end - 1 ? full_hi + 1 - TK : key_end - 1;
-    for (int part = 0; part < 2; ++part) {
-      const int stop = part || full_lo >= key_end ? key_end : (int)full_lo;
-      for (; key0 < stop; key0 += stride) masked_tile(key0);
-      if (part || key0 > full_end) continue;
-      fetch(key0);
-      resolve();
-      load_k();
-      load_v();
-      fetch(key0 + stride);
-      for (; key0 + stride <= full_end; key0 += stride) full_tile<true>(key0, stride);
-      full_tile<false>(key0, stride);
-      key0 += stride;
-    }
-    // the sums over the four lane groups of a row (their maxima are the same)
+  // Values that no row sees may be anything: they become zero.
+  __device__ __forceinline__ void drop(const Cursor& cur, uint32_t ok_now, int t0, int t1) {
+    const int last = cur.len - Q + t1;
+    const int64_t firsts = a.window ? (int64_t)cur.len - Q + t0 - a.window + 1 : 0;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      l[rt] += __shfl_xor(l[rt], 16, 64);
-      l[rt] += __shfl_xor(l[rt], 32, 64);
+    for (int i = 0; i < TK / 4; ++i) {
+      const int key = cur.key + key_of(i);
+      const bool see = key <= last && key >= firsts && ((ok_now >> key_of(i)) & 1u);
+#pragma unroll
+      for (int d = 0; d < VRow<NV, FP8>::kDw; ++d) vr[i].w[d] = see ? vr[i].w[d] : 0u;
+    }
+  }
+  // A key that some rows see and others do not has weight 0 for these, which is
+  // enough unless its value is infinite or NaN (0 * inf would reach them). Such
+  // a value becomes zero, and the sum of the rows that see it NaN. weightless:
+  // bit i, this lane's row does not see key i.
+  __device__ __forceinline__ void settle(const uint32_t (&weightless)[RT]) {
+#pragma unroll
+    for (int i = 0; i < TK / 4; ++i) {
+      const bool bad = vr[i].not_finite();
+#pragma unroll
+      for (int d = 0; d < VRow<NV, FP8>::kDw; ++d) vr[i].w[d] = bad ? 0u : vr[i].w[d];
+      const bool any = (__ballot(bad) >> (16 * g)) & 0xFFFFu;   // of the key's 16 lanes
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        if (any && !((weightless[rt] >> i) & 1u)) l[rt] = __builtin_nanf("");
+    }
+  }
+
+  // `count` (>= 1) tiles from cur on, `step` apart. While a tile is computed
+  // the next one is loaded (K while the values are multiplied, V while the
+  // next scores are), also across sequences. finish(cursor) where a
+  // sequence or the run ends, with O, m and l (summed over a row's lanes) of
+  // the tiles since the last one. One body for every kind of tile: code that
+  // runs once is paid for in instruction fetches.
+  template <typename F>
+  __device__ __forceinline__ void pass(Cursor cur, int count, int step, F finish) {
+    load_q(cur.b);
+    fetch(cur);
+    resolve();
+    load_k(true);
+    load_v(true);
+    Cursor nxt = after(cur, step);
+    fetch(nxt);
+    const int t0 = row0 / G, t1 = (row0 + rows - 1) / G;   // the rows' tokens
+    for (;;) {
+      const bool more = --count > 0;
+      f32x4_t S[RT][NU];
+      u32x4_t pf[RT][NP];
+      scores(S);
+      const uint32_t ok_now = ok;
+      resolve();
+      load_k(more);
+      const Cursor nxt2 = after(nxt, step);
+      fetch(nxt2);
+      // every row sees the whole tile
+      const int pos0 = cur.len - Q;
+      const bool all = ok_now == kAll && cur.key + TK - 1 <= pos0 &&
+                       (!a.window || cur.key >= (int64_t)cur.len - a.window);
+      uint32_t weightless[RT];
+      if (!all) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const int hi = tok[rt] < 0 ? -1 : pos0 + tok[rt];
+          const int64_t lo = a.window ? (int64_t)hi - a.window + 1 : 0;
+          weightless[rt] = 0u;
+#pragma unroll
+          for (int e = 0; e < 4 * NU; ++e) {
+            const int key = cur.key + key_of(e);
+            if (key > hi || key < lo || !((ok_now >> key_of(e)) & 1u)) {
+              S[rt][e >> 2][e & 3] = -INFINITY;
+              weightless[rt] |= 1u << e;
+            }
+          }
+        }
+      }
+      softmax(S, pf);
+      if (!all) {
+        drop(cur, ok_now, t0, t1);
+        if (t1 > t0) settle(weightless);
+      }
+      values(pf);
+      load_v(more);
+      if (!more || nxt.b != cur.b) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {   // a row's four lanes (their maxima are the same)
+          l[rt] += __shfl_xor(l[rt], 16, 64);
+          l[rt] += __shfl_xor(l[rt], 32, 64);
+        }
+        finish(cur);
+        if (!more) break;
+        clear();
+        load_q(nxt.b);
+        // here, on the rare path: otherwise every tile would wait for queries
+        // that may be in flight, and with them for its successor
+        __builtin_amdgcn_s_waitcnt(kVmcnt0);
+      }
+      cur = nxt;
+      nxt = nxt2;
     }
   }
 
   // O^T row g * 4 + i of the products is dims (g * 4 + i) * 8 .. + 7 (heads of
-  // 64: * 4 .. + 3; of 256: products 8 .. 15 are the second half). f(rt, d0,
-  // v): 4 consecutive dims of row rt * 16 + n.
+  // 64: * 4 .. + 3; of 256: products 8 .. 15 are the second half). f(d0, v): 4
+  // consecutive dims of row rt * 16 + n.
   template <typename F>
-  __device__ __forceinline__ void each4(F f) const {
+  __device__ __forceinline__ void each4(int rt, F f) const {
     constexpr int kRun = NV > 8 ? 8 : NV;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int t = 0; t < NV; t += 4)
-          f(rt, (t / kRun) * 128 + (g * 4 + i) * kRun + t % kRun,
+      for (int t = 0; t < NV; t += 4)
+          f((t / kRun) * 128 + (g * 4 + i) * kRun + t % kRun,
             f32x4_t{O[rt][t][i], O[rt][t + 1][i], O[rt][t + 2][i], O[rt][t + 3][i]});
   }
 };
@@ -514,52 +580,45 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4_t v) {
 
 // The split form: a wavefront per (run, head).
 template <int D, bool FP8, int RT, bool PG>
-__global__ __launch_bounds__(256, waves_per_simd(RT, D)) void k_attn_runs(const AttnArgs a,
+__global__ __launch_bounds__(256, waves_per_simd(RT, D, FP8)) void k_attn_runs(const AttnArgs a,
                                                                           const AttnShape sh) {
-  constexpr int TK = tile_keys(D, FP8);
-  const int total = total_tiles<TK>(a, sh);
-  const Runs runs(total, sh.groups);
+  const Tiles tiles(a, sh);
+  const Runs runs(tiles.total, sh.groups);
   const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int w = unit / sh.NHV, hv = unit - w * sh.NHV;
   if (w >= runs.nw) return;
   const int rt_tile = hv / (int)a.Hkv, h = hv - rt_tile * (int)a.Hkv;
-  int s = runs.start(w);
-  const int s_end = runs.start(w + 1);
-  int before;
-  int b = find_sequence<TK>(a, sh, s, before);
-  int s_in = s - before;
-  const const_i32 lens = (const_i32)(uintptr_t)a.lens;
+  const int s = runs.start(w), count = runs.start(w + 1) - s;
+  int before, len;
+  const int b = tiles.find(s, before, len);
   const float ks = FP8 ? *a.k_scale : 1.0f, vs = FP8 ? *a.v_scale : 1.0f;
-  for (bool first = true; s < s_end; first = false, ++b, s_in = 0) {
-    const Span sp = span_of<TK>(a, sh, lens[b]);
-    const int e_in = sp.n - s_in < s_end - s ? sp.n : s_in + (s_end - s);
-    AttnWave<D, FP8, RT, PG, TK> wave(a, sh, b, h, rt_tile * (RT * 16), sp, a.scale * ks * kLog2e);
-    const int end = sp.base + e_in * TK;
-    wave.pass(sp.base + s_in * TK, end < sp.len ? end : sp.len, TK);
-    const bool whole = s_in == 0 && e_in == sp.n;
-    const int64_t rec = ((int64_t)(w * sh.NHV + hv) * 2 + (first ? 0 : 1)) * sh.slot_rows;
-    float f[RT];
-    uint16_t* out[RT];
+  AttnWave<D, FP8, RT, PG> wave(a, sh, h, rt_tile * (RT * 16), a.scale * ks * kLog2e);
+  bool from_start = s == before;
+  int64_t rec = (int64_t)(w * sh.NHV + hv) * 2 * sh.slot_rows;
+  wave.pass(wave.first_of(b, len, s - before), count, 1, [&](const Cursor& c) {
+    const bool whole = from_start && c.left == 1;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      f[rt] = wave.l[rt] == 0.0f ? 0.0f : vs / wave.l[rt];
-      const int r = wave.row0 + rt * 16 + wave.n;
-      out[rt] = a.out + ((int64_t)(b * a.Q + wave.tok[rt]) * a.Hq + h * sh.G +
-                         (r - wave.tok[rt] * sh.G)) * D;
-      if (!whole && wave.tok[rt] >= 0 && wave.g == 0) {
-        sh.ml[(rec + rt * 16 + wave.n) * 2] = wave.m[rt];
-        sh.ml[(rec + rt * 16 + wave.n) * 2 + 1] = wave.l[rt];
+      if (wave.tok[rt] < 0) continue;
+      const int r = rt * 16 + wave.n;
+      if (whole) {
+        const float f = wave.l[rt] == 0.0f ? 0.0f : vs / wave.l[rt];
+        uint16_t* o = a.out + ((int64_t)(c.b * a.Q + wave.tok[rt]) * a.Hq + h * sh.G +
+                               (wave.row0 + r - wave.tok[rt] * sh.G)) * D;
+        wave.each4(rt, [&](int d, f32x4_t v) { store4(o + d, v * f); });
+      } else {
+        if (wave.g == 0) {
+          sh.ml[(rec + r) * 2] = wave.m[rt];
+          sh.ml[(rec + r) * 2 + 1] = wave.l[rt];
+        }
+        float* o = sh.o + (rec + r) * D;
+        wave.each4(rt, [&](int d, f32x4_t v) { *reinterpret_cast<f32x4_t*>(o + d) = v; });
       }
     }
-    wave.each4([&](int rt, int d, f32x4_t v) {
-      if (wave.tok[rt] < 0) return;
-      if (whole)
-        store4(out[rt] + d, v * f[rt]);
-      else
-        *reinterpret_cast<f32x4_t*>(sh.o + (rec + rt * 16 + wave.n) * D + d) = v;
-    });
-    s += e_in - s_in;
-  }
+    // only a run's first and last parts can be records
+    rec = ((int64_t)(w * sh.NHV + hv) * 2 + 1) * sh.slot_rows;
+    from_start = true;
+  });
 }
 
 // The whole form: a workgroup per (sequence, head); its wavefronts take the
@@ -567,26 +626,27 @@ __global__ __launch_bounds__(256, waves_per_simd(RT, D)) void k_attn_runs(const 
 template <int D, bool FP8, int RT, bool PG>
 __global__ __launch_bounds__(kWholeWaves * 64, 2) void k_attn_whole(const AttnArgs a,
                                                                     const AttnShape sh) {
-  constexpr int TK = 32;
   __shared__ float lds_o[kWholeWaves][RT * 16][D + 4];
   __shared__ float lds_ml[kWholeWaves][RT * 16][2];
   const int b = blockIdx.x / sh.NHV, hv = blockIdx.x - b * sh.NHV;
   const int rt_tile = hv / (int)a.Hkv, h = hv - rt_tile * (int)a.Hkv;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float ks = FP8 ? *a.k_scale : 1.0f, vs = FP8 ? *a.v_scale : 1.0f;
-  const const_i32 lens = (const_i32)(uintptr_t)a.lens;
-  const Span sp = span_of<TK>(a, sh, lens[b]);
-  AttnWave<D, FP8, RT, PG, TK> wave(a, sh, b, h, rt_tile * (RT * 16), sp, a.scale * ks * kLog2e);
-  wave.pass(sp.base + wv * TK, sp.len, kWholeWaves * TK);
+  const int len = ((const_i32)(uintptr_t)a.lens)[b];
+  AttnWave<D, FP8, RT, PG> wave(a, sh, h, rt_tile * (RT * 16), a.scale * ks * kLog2e);
+  const int count = (span_of(a, sh, len).n - wv + kWholeWaves - 1) / kWholeWaves;
+  if (count > 0) wave.pass(wave.first_of(b, len, wv), count, kWholeWaves, [](const Cursor&) {});
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
     if (wave.g == 0) {
       lds_ml[wv][rt * 16 + wave.n][0] = wave.m[rt];
       lds_ml[wv][rt * 16 + wave.n][1] = wave.l[rt];
     }
-  wave.each4([&](int rt, int d, f32x4_t v) {
-    *reinterpret_cast<f32x4_t*>(&lds_o[wv][rt * 16 + wave.n][d]) = v;
-  });
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+    wave.each4(rt, [&](int d, f32x4_t v) {
+      *reinterpret_cast<f32x4_t*>(&lds_o[wv][rt * 16 + wave.n][d]) = v;
+    });
   __syncthreads();
   for (int it = threadIdx.x; it < wave.rows * (D / 8); it += kWholeWaves * 64) {
     const int r = it / (D / 8), d0 = (it % (D / 8)) * 8;
@@ -611,69 +671,73 @@ __global__ __launch_bounds__(kWholeWaves * 64, 2) void k_attn_whole(const AttnAr
 }
 
 // One workgroup per (sequence, head, row) of a sequence that several runs
-// share: groups of D / 4 threads take its partial records in turn,
-// then meet in LDS.
-template <int D, int TK>
+// share: the records' weights first, then groups of D / 4 threads add the
+// records in turn and meet in LDS.
+template <int D>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnShape sh) {
   constexpr int TD = D / 4, NG = 256 / TD;
   __shared__ float lds[NG][D + 4];
-  __shared__ float lds_ml[NG][2];
+  __shared__ float lds_f[kMaxRuns];
+  __shared__ float lds_red[2][4];
   const int b = blockIdx.x / sh.NHV, hv = blockIdx.x % sh.NHV, r = blockIdx.y;
   const int rt_tile = hv / (int)a.Hkv, h = hv - rt_tile * (int)a.Hkv;
   const int rr = rt_tile * sh.slot_rows + r;
   if (rr >= sh.rows) return;
+  const Tiles tiles(a, sh);
+  const Runs runs(tiles.total, sh.groups);
+  const int s0 = tiles.before(b), nb = span_of(a, sh, a.lens[b]).n;
   const int lane = threadIdx.x & 63;
-  // steps before this sequence, and all of them
-  int bef = 0, tot = 0;
-  for (int i = lane; i < (int)a.B; i += 64) {
-    const int n = span_of<TK>(a, sh, a.lens[i]).n;
-    tot += n;
-    bef += i < b ? n : 0;
-  }
-  const int total = wave_sum_i32(tot), s0 = wave_sum_i32(bef);
-  const int nb = span_of<TK>(a, sh, a.lens[b]).n;
-  const Runs runs(total, sh.groups);
   const int w0 = runs.of(s0), w1 = runs.of(s0 + nb - 1);
   if (w0 == w1) return;   // finished by its one wavefront
-  const int grp = threadIdx.x / TD, d0 = (threadIdx.x % TD) * 4;
-  float m = -INFINITY, l = 0.0f;
-  f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int w = w0 + grp; w <= w1; w += NG) {
-    // a run that starts inside this sequence, or with it, has it as its first
-    // part
-    const int64_t slot = ((int64_t)w * sh.NHV + hv) * 2 + (w > w0 || runs.start(w) == s0 ? 0 : 1);
-    const int64_t rec = slot * sh.slot_rows + r;
-    const float mw = sh.ml[rec * 2], lw = sh.ml[rec * 2 + 1];
-    const f32x4_t ow = *reinterpret_cast<const f32x4_t*>(sh.o + rec * D + d0);
-    const float mn = fmaxf(m, mw);
-    const float use = mn == -INFINITY ? 0.0f : mn;
-    const float f0 = __builtin_amdgcn_exp2f(m - use), f1 = __builtin_amdgcn_exp2f(mw - use);
-    l = l * f0 + lw * f1;
+  // a run that starts inside this sequence, or with it, has it as its first
+  // part
+  const int odd = runs.start(w0) == s0 ? 0 : 1;
+  auto record = [&](int i) {
+    return (((int64_t)(w0 + i) * sh.NHV + hv) * 2 + (i == 0 ? odd : 0)) * sh.slot_rows + r;
+  };
+  // the records' weights against their largest maximum, and the sum
+  const int np = w1 - w0 + 1, wv = threadIdx.x >> 6;
+  float mx = -INFINITY;
+  for (int i = threadIdx.x; i < np; i += 256) {
+    const float m = sh.ml[record(i) * 2];
+    lds_f[i] = m;
+    mx = fmaxf(mx, m);
+  }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = o[e] * f0 + ow[e] * f1;
-    m = mn;
+  for (int o = 32; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 64));
+  if (lane == 0) lds_red[0][wv] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(lds_red[0][0], lds_red[0][1]), fmaxf(lds_red[0][2], lds_red[0][3]));
+  const float use = mx == -INFINITY ? 0.0f : mx;
+  float l = 0.0f;
+  for (int i = threadIdx.x; i < np; i += 256) {
+    const float f = __builtin_amdgcn_exp2f(lds_f[i] - use);
+    lds_f[i] = f;
+    l = fmaf(sh.ml[record(i) * 2 + 1], f, l);
+  }
+  l = wave_sum(l);
+  if (lane == 0) lds_red[1][wv] = l;
+  __syncthreads();
+  l = (lds_red[1][0] + lds_red[1][1]) + (lds_red[1][2] + lds_red[1][3]);
+  const int grp = threadIdx.x / TD, d0 = (threadIdx.x % TD) * 4;
+  f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int i = grp; i < np; i += NG) {
+    const f32x4_t ow = *reinterpret_cast<const f32x4_t*>(sh.o + record(i) * D + d0);
+    const float f = lds_f[i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = fmaf(ow[e], f, o[e]);
   }
   *reinterpret_cast<f32x4_t*>(&lds[grp][d0]) = o;
-  if (d0 == 0) {
-    lds_ml[grp][0] = m;
-    lds_ml[grp][1] = l;
-  }
   __syncthreads();
   if (threadIdx.x >= D / 8) return;
   const int d = threadIdx.x * 8;
-  float mm = -INFINITY;
+  const float f = l == 0.0f ? 0.0f : (a.cache_e4m3 ? *a.v_scale : 1.0f) / l;
+  float out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-  for (int v = 0; v < NG; ++v) mm = fmaxf(mm, lds_ml[v][0]);
-  const float use = mm == -INFINITY ? 0.0f : mm;
-  float ll = 0.0f, out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  for (int v = 0; v < NG; ++v)
 #pragma unroll
-  for (int v = 0; v < NG; ++v) {
-    const float f = __builtin_amdgcn_exp2f(lds_ml[v][0] - use);
-    ll = fmaf(lds_ml[v][1], f, ll);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) out[e] = fmaf(lds[v][d + e], f, out[e]);
-  }
-  const float f = ll == 0.0f ? 0.0f : (a.cache_e4m3 ? *a.v_scale : 1.0f) / ll;
+    for (int e = 0; e < 8; ++e) out[e] += lds[v][d + e];
 #pragma unroll
   for (int e = 0; e < 8; ++e) out[e] *= f;
   const int t = rr / sh.G;
@@ -690,13 +754,14 @@ struct AttnLayout {
   size_t ml, o, total;
   int RT, slot_rows, NHV, groups;
 };
-AttnLayout attn_layout(int64_t rows, int64_t Hkv, int64_t D) {
+AttnLayout attn_layout(int64_t rows, int64_t Hkv, int64_t D, bool e4m3) {
   AttnLayout L;
   L.RT = row_tiles(rows, D);
   L.NHV = (int)(Hkv * ((rows + L.RT * 16 - 1) / (L.RT * 16)));
   L.slot_rows = (int)(rows < L.RT * 16 ? rows : L.RT * 16);
-  L.groups = kCus * 4 * waves_per_simd(L.RT, (int)D) / L.NHV;
+  L.groups = kCus * 4 * waves_per_simd(L.RT, (int)D, e4m3) / L.NHV;
   if (L.groups < 1) L.groups = 1;
+  if (L.groups > kMaxRuns) L.groups = kMaxRuns;
   const size_t slots = (size_t)2 * L.groups * L.NHV;
   L.ml = 0;
   L.o = (slots * L.slot_rows * 2 * sizeof(float) + 255) & ~(size_t)255;
@@ -718,9 +783,11 @@ int64_t most_keys(const AttnArgs& a) {
 
 template <int D, bool FP8, int RT, bool PG>
 hipError_t launch_rt(const AttnArgs& a, AttnShape& sh, const AttnLayout& L, hipStream_t stream) {
-  constexpr int TK = tile_keys(D, FP8);
   constexpr bool kFits = (size_t)kWholeWaves * RT * 16 * (D + 6) * 4 <= 160 * 1024;
   const int64_t keys = most_keys(a);
+  // no page at all: every sequence is empty
+  if (sh.cap == 0)
+    return launch_fill_zero((float*)a.out, (size_t)(a.B * a.Q * a.Hq * D / 2), stream);
   if constexpr (kFits) {
     if (keys <= kWholeKeys) {
       hipLaunchKernelGGL((k_attn_whole<D, FP8, RT, PG>), dim3((uint32_t)(a.B * sh.NHV)),
@@ -736,7 +803,7 @@ hipError_t launch_rt(const AttnArgs& a, AttnShape& sh, const AttnLayout& L, hipS
                      0, stream, a, sh);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || keys <= TK) return e;   // a sequence of one tile is never shared
-  hipLaunchKernelGGL((k_attn_join<D, TK>),
+  hipLaunchKernelGGL((k_attn_join<D>),
                      dim3((uint32_t)(a.B * sh.NHV), (uint32_t)sh.slot_rows), dim3(256), 0, stream,
                      a, sh);
   return hipGetLastError();
@@ -747,7 +814,7 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
   AttnShape sh;
   sh.G = (int)(a.Hq / a.Hkv);
   sh.rows = sh.G * (int)a.Q;
-  const AttnLayout L = attn_layout(sh.rows, a.Hkv, D);
+  const AttnLayout L = attn_layout(sh.rows, a.Hkv, D, FP8);
   sh.NHV = L.NHV;
   sh.cap = capacity(a);
   sh.page_shift = (a.page & (a.page - 1)) == 0 ? __builtin_ctzll((uint64_t)a.page) : -1;
@@ -770,7 +837,10 @@ bool attn_fits(const AttnArgs& a) { return (most_keys(a) + 31) / 32 * a.B < 0x7F
 
 size_t attn_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv, int64_t D) {
   if (B == 0 || Q == 0) return 0;
-  return attn_layout(Hq / Hkv * Q, Hkv, D).total;
+  // the call's cache type is not known here: the larger of the two
+  const size_t n = attn_layout(Hq / Hkv * Q, Hkv, D, false).total;
+  const size_t m = attn_layout(Hq / Hkv * Q, Hkv, D, true).total;
+  return n > m ? n : m;
 }
 
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream) {
