@@ -644,8 +644,10 @@ size_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, i
  *
  * with G = Hq / Hkv. A token that sees no key (seq_lens[b] <= 0, or p < 0)
  * gives zeros. A key or value that a token does not see does not reach it,
- * whatever its bits are (NaN and infinities included). Scores, maxima and
- * sums are fp32; the probabilities are rounded to bf16 for the product with V.
+ * whatever its bits are (NaN and infinities included). An infinite or NaN
+ * value that some of the Q tokens see and others do not gives NaN for those
+ * that do. Scores, maxima and sums are fp32; the probabilities enter the
+ * product with V as the sum of two bf16 (16 bits).
  *
  *   q            bf16[B * Q, Hq, D] (uint16 bits), 16-byte aligned;
  *   cache        bf16 or E4M3, D 64, 128 or 256;
@@ -662,8 +664,9 @@ size_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, i
  *                D) bytes, 256-byte aligned; overwritten, its content does
  *                not matter; must not be shared by calls that may run
  *                concurrently.
- * One launch, or two where a sequence may be longer than 128 keys. The work is
- * divided on the device by the lengths, so a captured call follows them.
+ * One launch where the table's rows (or the window) hold few keys, else two.
+ * The work is divided on the device by the lengths, so a captured call follows
+ * them.
  * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, WORKSPACE, ALIAS, HIP.
  */
 nvfp4_status nvfp4_paged_attention(const uint16_t* q, const nvfp4_kv_cache* cache,

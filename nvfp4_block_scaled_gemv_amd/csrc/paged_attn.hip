@@ -38,15 +38,19 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kCus = 256;
+// The whole form: sequences of at most kWholeKeys keys, twice that where there
+// are kWholeMany workgroups or more. One sequence (32 / 8 heads of 128, bf16,
+// between two events): 12.4 us against 15.2 in two launches at 256 keys, 14.8
+// against 15.8 at 512, 18.8 against 16.1 at 1024; 64 of them at 1024: 56.7
+// against 55.6; 8 with 4 tokens each at 1024 (E4M3): 18.8 against 29.1.
 constexpr int kWholeWaves = 8;
-constexpr int kWholeKeys = 1024;
+constexpr int kWholeKeys = 512;
+constexpr int kWholeMany = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 // The reference of the exponentials is moved only when a score passes it by
 // more than this (in powers of two): exp2 of at most 2^8 loses nothing in fp32
 // or bf16, and most turns need no maximum across lanes and no rescaling.
 constexpr float kSlack = 8.0f;
-// A run has at least this many tiles: fewer records to join.
-constexpr int kMinTiles = 1;
 // s_waitcnt vmcnt(0), no other counter.
 constexpr int kVmcnt0 = 0x0F70;
 // Runs of one head at most.
@@ -152,12 +156,11 @@ struct Tiles {
   }
 };
 // Run w starts at tile start(w); the first r runs have q + 1 tiles and the
-// others q (total = nw * q + r). of(s): the run that has tile s.
+// others q (nw * q + r in all). of(s): the run that has tile s.
 struct Runs {
   int nw, q, r;
   __device__ __forceinline__ Runs(int total, int groups) {
-    nw = (total + kMinTiles - 1) / kMinTiles;
-    nw = nw < groups ? nw : groups;
+    nw = total < groups ? total : groups;
     q = total / nw;
     r = total % nw;
   }
@@ -367,7 +370,11 @@ struct AttnWave {
       const uint8_t* p = PG ? kc + off[PG ? u : 0] * ES + lane_off
                             : want ? kc + at_key(off, 16 * u + n) + g * 16 : kc;
 #pragma unroll
-      for (int j = 0; j < KL; ++j) kr[u][j] = load_stream(p + j * 64);
+      for (int j = 0; j < KL; ++j)
+        // a load takes 64 bytes of a key: half of an E4M3 head of 128, whose
+        // other half the hint would read again (6.1 against 5.9 TB/s); wider
+        // rows want the hint (bf16: 6.6 against 6.4)
+        kr[u][j] = FP8 ? *reinterpret_cast<const u32x4_t*>(p + j * 64) : load_stream(p + j * 64);
     }
   }
   __device__ __forceinline__ void load_v(bool want) {
@@ -404,8 +411,9 @@ struct AttnWave {
       for (int rt = 0; rt < RT; ++rt) S[rt][u] *= c;
     }
   }
-  // The running maximum and sum, and P as bf16 pairs.
-  __device__ __forceinline__ void softmax(const f32x4_t (&S)[RT][NU], u32x4_t (&pf)[RT][NP]) {
+  // The running maximum and sum, and P as the sum of two bf16: in one, its
+  // rounding (2^-9 of each weight) would be as large as the output's own.
+  __device__ __forceinline__ void softmax(const f32x4_t (&S)[RT][NU], u32x4_t (&pf)[RT][NP], u32x4_t (&pl)[RT][NP]) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       float mx = -INFINITY;
@@ -427,7 +435,9 @@ struct AttnWave {
         const float p0 = __builtin_amdgcn_exp2f(S[rt][e >> 1][(e & 1) * 2] - m_use);
         const float p1 = __builtin_amdgcn_exp2f(S[rt][e >> 1][(e & 1) * 2 + 1] - m_use);
         l[rt] += p0 + p1;
-        pf[rt][e >> 2][e & 3] = pack_bf16(p0, p1);
+        const uint32_t top = pack_bf16(p0, p1);
+        pf[rt][e >> 2][e & 3] = top;
+        pl[rt][e >> 2][e & 3] = pack_bf16(p0 - bf16_lo(top), p1 - bf16_hi(top));
       }
     }
   }
@@ -436,7 +446,7 @@ struct AttnWave {
                                                    __builtin_bit_cast(bf16x8_t, pf), acc, 0, 0, 0);
   }
   // O += V^T P^T
-  __device__ __forceinline__ void values(const u32x4_t (&pf)[RT][NP]) {
+  __device__ __forceinline__ void values(const u32x4_t (&pf)[RT][NP], const u32x4_t (&pl)[RT][NP]) {
 #pragma unroll
     for (int d = 0; d < NV / 2; ++d) {
 #pragma unroll
@@ -450,6 +460,8 @@ struct AttnWave {
                             perm_hi(x[6], x[7])};
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
+          O[rt][2 * d] = product(lo, pl[rt][q], O[rt][2 * d]);
+          O[rt][2 * d + 1] = product(hi, pl[rt][q], O[rt][2 * d + 1]);
           O[rt][2 * d] = product(lo, pf[rt][q], O[rt][2 * d]);
           O[rt][2 * d + 1] = product(hi, pf[rt][q], O[rt][2 * d + 1]);
         }
@@ -505,7 +517,7 @@ struct AttnWave {
     for (;;) {
       const bool more = --count > 0;
       f32x4_t S[RT][NU];
-      u32x4_t pf[RT][NP];
+      u32x4_t pf[RT][NP], pl[RT][NP];
       scores(S);
       const uint32_t ok_now = ok;
       resolve();
@@ -533,12 +545,12 @@ struct AttnWave {
           }
         }
       }
-      softmax(S, pf);
+      softmax(S, pf, pl);
       if (!all) {
         drop(cur, ok_now, t0, t1);
         if (t1 > t0) settle(weightless);
       }
-      values(pf);
+      values(pf, pl);
       load_v(more);
       if (!more || nxt.b != cur.b) {
 #pragma unroll
@@ -695,8 +707,16 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnS
   auto record = [&](int i) {
     return (((int64_t)(w0 + i) * sh.NHV + hv) * 2 + (i == 0 ? odd : 0)) * sh.slot_rows + r;
   };
-  // the records' weights against their largest maximum, and the sum
   const int np = w1 - w0 + 1, wv = threadIdx.x >> 6;
+  // the first records' values are on their way while the weights are made
+  constexpr int kEarly = 4;
+  const int grp = threadIdx.x / TD, d0 = (threadIdx.x % TD) * 4;
+  f32x4_t early[kEarly];
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+    if (grp + k * NG < np)
+      early[k] = *reinterpret_cast<const f32x4_t*>(sh.o + record(grp + k * NG) * D + d0);
+  // the records' weights against their largest maximum, and the sum
   float mx = -INFINITY;
   for (int i = threadIdx.x; i < np; i += 256) {
     const float m = sh.ml[record(i) * 2];
@@ -719,15 +739,17 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnS
   if (lane == 0) lds_red[1][wv] = l;
   __syncthreads();
   l = (lds_red[1][0] + lds_red[1][1]) + (lds_red[1][2] + lds_red[1][3]);
-  const int grp = threadIdx.x / TD, d0 = (threadIdx.x % TD) * 4;
   f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
-  for (int i = grp; i < np; i += NG) {
-    const f32x4_t ow = *reinterpret_cast<const f32x4_t*>(sh.o + record(i) * D + d0);
-    const float f = lds_f[i];
+  auto add = [&](f32x4_t ow, float f) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = fmaf(ow[e], f, o[e]);
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+    if (grp + k * NG < np) add(early[k], lds_f[grp + k * NG]);
+#pragma unroll 8
+  for (int i = grp + kEarly * NG; i < np; i += NG)
+    add(*reinterpret_cast<const f32x4_t*>(sh.o + record(i) * D + d0), lds_f[i]);
   *reinterpret_cast<f32x4_t*>(&lds[grp][d0]) = o;
   __syncthreads();
   if (threadIdx.x >= D / 8) return;
@@ -783,13 +805,12 @@ int64_t most_keys(const AttnArgs& a) {
 
 template <int D, bool FP8, int RT, bool PG>
 hipError_t launch_rt(const AttnArgs& a, AttnShape& sh, const AttnLayout& L, hipStream_t stream) {
-  constexpr bool kFits = (size_t)kWholeWaves * RT * 16 * (D + 6) * 4 <= 160 * 1024;
   const int64_t keys = most_keys(a);
   // no page at all: every sequence is empty
   if (sh.cap == 0)
     return launch_fill_zero((float*)a.out, (size_t)(a.B * a.Q * a.Hq * D / 2), stream);
-  if constexpr (kFits) {
-    if (keys <= kWholeKeys) {
+  if constexpr (D < 256) {   // heads of 256: their eight wavefronts' registers would spill
+    if (keys <= kWholeKeys * (a.B * sh.NHV >= kWholeMany ? 2 : 1)) {
       hipLaunchKernelGGL((k_attn_whole<D, FP8, RT, PG>), dim3((uint32_t)(a.B * sh.NHV)),
                          dim3(kWholeWaves * 64), 0, stream, a, sh);
       return hipGetLastError();
