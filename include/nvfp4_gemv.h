@@ -658,7 +658,9 @@ size_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, i
  *                page counts as that;
  *   scale        the scores' factor, usually 1 / sqrt(D);
  *   B, Q         0 <= B <= NVFP4_ATTN_MAX_B, 0 <= Q <= NVFP4_ATTN_MAX_Q;
- *   Hq           a multiple of the cache's n_kv_heads, <= NVFP4_MAX_HEADS;
+ *   Hq           a multiple of the cache's n_kv_heads, <= NVFP4_MAX_HEADS. B *
+ *                n_kv_heads * (row tiles of 16 of the Hq / n_kv_heads * Q rows)
+ *                may be refused past 2^22;
  *   out          bf16[B * Q, Hq, D] out, 16-byte aligned;
  *   workspace    at least nvfp4_paged_attention_workspace_bytes(B, Q, Hq, Hkv,
  *                D) bytes, 256-byte aligned; overwritten, its content does

@@ -623,24 +623,52 @@ def moe_w4a4_workspace_layout(M: int, H: int, I: int, topk: int, I_shared: int =
 
 
 # ------------------------------------------------- between the GEMVs: norms
+# These calls take a few microseconds on the device, so their checks are kept
+# to what the C side cannot see, one attribute at a time.
+
+# The current device's index without the initialisation check of
+# torch.cuda.current_device (a device tensor is at hand wherever it is asked).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _same_device(d, *ts) -> None:
+    """Tensors (None is skipped) on the HIP device of index d (-1: none), which
+    must be the current one: the library launches there."""
+    if d < 0:
+        raise ValueError("tensors must be on a HIP device")
+    if d != _current_device():
+        raise ValueError(f"tensors are on device {d}, the current one is {_current_device()}")
+    for t in ts:
+        if t is not None and t.get_device() != d:
+            raise ValueError("tensors must be on one HIP device")
+
+
+def _contiguous(*ts) -> None:
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+
 
 def _norm_args(x, weight, residual, residual_out, *outs):
     """The arguments that the three norms share, checked."""
-    _dev(x, weight, residual, residual_out, *outs)
+    _same_device(x.get_device(), weight, residual, residual_out, *outs)
+    _contiguous(x, weight, residual, residual_out, *outs)
     xt = _ACT_TYPES.get(x.dtype)
     if xt is None or weight.dtype is not torch.bfloat16:
         raise TypeError(f"x must be bf16 or fp32 and weight bf16, got {x.dtype}, {weight.dtype}")
-    M, H = x.shape
+    M, H = shape = x.shape
     if weight.shape != (H,):
         raise ValueError(f"weight must have shape ({H},), got {tuple(weight.shape)}")
-    if (residual is None) != (residual_out is None):
-        raise ValueError("residual and residual_out go together")
     if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual and residual_out go together")
         return x.data_ptr(), xt, None, None, 0, weight.data_ptr(), M, H
+    if residual_out is None:
+        raise ValueError("residual and residual_out go together")
     rt = _ACT_TYPES.get(residual.dtype)
     if rt is None or residual_out.dtype is not residual.dtype:
         raise TypeError("residual must be bf16 or fp32, residual_out the same")
-    if residual.shape != x.shape or residual_out.shape != x.shape:
+    if residual.shape != shape or residual_out.shape != shape:
         raise ValueError("residual and residual_out must have x's shape")
     return (x.data_ptr(), xt, residual.data_ptr(), residual_out.data_ptr(), rt,
             weight.data_ptr(), M, H)
@@ -740,13 +768,6 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale) -> KvCache:
                    ct)
 
 
-def _same_device(d, *ts):
-    """Tensors (None is skipped) on the HIP device of index d."""
-    for t in ts:
-        if t is not None and (not t.is_cuda or t.get_device() != d):
-            raise ValueError("tensors must be on one HIP device")
-
-
 def rope_append_into(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache, k_scale=None,
                      v_scale=None, interleaved: bool = False, rope_scale: float = 1.0) -> None:
     """Rotary positions of q[T, Hq, D] and k[T, Hkv, D] (bf16 or fp32; a
@@ -760,8 +781,8 @@ def rope_append_into(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cach
     x = k if q is None else q
     if x is None:
         raise ValueError("neither q nor k is given")
-    d = x.get_device()
-    _same_device(d, q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache, k_scale, v_scale)
+    _same_device(x.get_device(), q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache,
+                 k_scale, v_scale)
     xt = _ACT_TYPES.get(x.dtype)
     if xt is None:
         raise TypeError(f"q, k and v must be bf16 or fp32, got {x.dtype}")
@@ -827,14 +848,12 @@ def paged_attention_into(q, k_cache, v_cache, block_table, seq_lens, out, worksp
     block_table int32 [B, max_blocks]; seq_lens int32 [B], the new tokens
     included; scale defaults to D ** -0.5; window > 0: each token sees the
     last `window` keys up to itself."""
-    d = q.get_device()
-    _same_device(d, q, k_cache, v_cache, block_table, seq_lens, out, workspace, k_scale, v_scale)
+    _same_device(q.get_device(), k_cache, v_cache, block_table, seq_lens, out, workspace, k_scale,
+                 v_scale)
     if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 \
             or block_table.dtype is not torch.int32 or seq_lens.dtype is not torch.int32:
         raise TypeError("q and out must be bf16, block_table and seq_lens int32")
-    if not (q.is_contiguous() and out.is_contiguous() and block_table.is_contiguous()
-            and seq_lens.is_contiguous() and workspace.is_contiguous()):
-        raise ValueError("q, out, block_table, seq_lens and workspace must be contiguous")
+    _contiguous(q, out, block_table, seq_lens, workspace)
     c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
     T, Hq, D = q.shape
     B, width = block_table.shape
@@ -845,8 +864,7 @@ def paged_attention_into(q, k_cache, v_cache, block_table, seq_lens, out, worksp
     _check("nvfp4_paged_attention", lib().nvfp4_paged_attention(
         q.data_ptr(), ctypes.byref(c), block_table.data_ptr(), seq_lens.data_ptr(), B,
         T // B if B else 0, Hq, width, D ** -0.5 if scale is None else scale, window,
-        out.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _stream(q)))
+        out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(q)))
 
 
 def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale: float | None = None,
@@ -876,7 +894,10 @@ def verify_draft_into(target_p, draft_p, draft, u_accept, u_sample, tokens, n_ac
     fp32 [B, Q] and u_sample fp32 [B] in [0, 1); n_draft int32 [B]: how many
     of the drafts are real (None: all). tokens int32 [B, Q + 1]: the kept
     drafts, the token drawn after them, then -1; n_accepted int32 [B]."""
-    _dev(target_p, draft_p, draft, u_accept, u_sample, tokens, n_accepted, workspace, n_draft)
+    _same_device(target_p.get_device(), draft_p, draft, u_accept, u_sample, tokens, n_accepted,
+                 workspace, n_draft)
+    _contiguous(target_p, draft_p, draft, u_accept, u_sample, tokens, n_accepted, workspace,
+                n_draft)
     f, i = torch.float32, torch.int32
     if target_p.dtype is not f or (draft_p is not None and draft_p.dtype is not f) \
             or u_accept.dtype is not f or u_sample.dtype is not f or draft.dtype is not i \
@@ -894,7 +915,7 @@ def verify_draft_into(target_p, draft_p, draft, u_accept, u_sample, tokens, n_ac
     _check("nvfp4_verify_draft", lib().nvfp4_verify_draft(
         target_p.data_ptr(), _p(draft_p), draft.data_ptr(), _p(n_draft), u_accept.data_ptr(),
         u_sample.data_ptr(), B, Q, V, tokens.data_ptr(), n_accepted.data_ptr(),
-        workspace.data_ptr(), workspace.numel() * workspace.element_size(), _stream(target_p)))
+        workspace.data_ptr(), workspace.nbytes, _stream(target_p)))
 
 
 def verify_draft(target_p, draft_p, draft, u_accept, u_sample, n_draft=None,

@@ -538,13 +538,16 @@ nvfp4_status cache_checks(const char* fn, const nvfp4_kv_cache& c) {
                 "%s: cache num_blocks=%lld page=%lld heads=%lld D=%lld stride_token=%lld is past a "
                 "limit", fn, (long long)c.num_blocks, (long long)c.page, (long long)c.n_kv_heads,
                 (long long)c.D, (long long)c.stride_token);
+  // the scales are read also where there is no page
+  if (c.type == NVFP4_E4M3 && (!c.k_scale || !c.v_scale))
+    return fail(NVFP4_ERR_NULL, "%s: an E4M3 cache needs k_scale and v_scale", fn);
+  if (c.type == NVFP4_E4M3 && (!aligned(c.k_scale, 4) || !aligned(c.v_scale, 4)))
+    return fail(NVFP4_ERR_ALIGN, "%s: k_scale and v_scale must be 4-byte aligned", fn);
   if (c.num_blocks == 0) return NVFP4_OK;
-  if (!c.k || !c.v || c.k == c.v || (c.type == NVFP4_E4M3 && (!c.k_scale || !c.v_scale)))
-    return fail(NVFP4_ERR_NULL, "%s: the cache's k and v (and an E4M3 cache's scales) must be "
-                "non-NULL and differ", fn);
-  if (!aligned(c.k, 16) || !aligned(c.v, 16) ||
-      (c.type == NVFP4_E4M3 && (!aligned(c.k_scale, 4) || !aligned(c.v_scale, 4))))
-    return fail(NVFP4_ERR_ALIGN, "%s: the cache must be 16-byte aligned, its scales 4-byte", fn);
+  if (!c.k || !c.v || c.k == c.v)
+    return fail(NVFP4_ERR_NULL, "%s: the cache's k and v must be non-NULL and differ", fn);
+  if (!aligned(c.k, 16) || !aligned(c.v, 16))
+    return fail(NVFP4_ERR_ALIGN, "%s: the cache must be 16-byte aligned", fn);
   return NVFP4_OK;
 }
 
@@ -719,7 +722,8 @@ nvfp4_status nvfp4_paged_attention(const uint16_t* q, const nvfp4_kv_cache* cach
   a.window = window;
   if (!nvfp4::attn_fits(a))
     return fail(NVFP4_ERR_UNSUPPORTED,
-                "%s: B * max_blocks * page has more than 2^31 tiles of 32 keys", fn);
+                "%s: more than 2^31 tiles of 32 keys (B * max_blocks * page), or than 2^22 "
+                "sequences times row tiles of all heads", fn);
   if (!q || !seq_lens || !out || (max_blocks && !block_table))
     return fail(NVFP4_ERR_NULL, "%s: NULL pointer", fn);
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4))

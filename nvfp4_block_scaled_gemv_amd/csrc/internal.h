@@ -202,7 +202,7 @@ struct AttnArgs {
   uint16_t* out;                     // bf16 [B * Q, Hq, D]
   void* workspace;
 };
-// its tiles of keys can be numbered in 31 bits
+// its tiles of keys and its launches stay within their 31 and 32 bits
 bool attn_fits(const AttnArgs& a);
 size_t attn_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv, int64_t D);
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream);

@@ -709,7 +709,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnS
   };
   const int np = w1 - w0 + 1, wv = threadIdx.x >> 6;
   // the first records' values are on their way while the weights are made
-  constexpr int kEarly = 4;
+  constexpr int kEarly = 8;
   const int grp = threadIdx.x / TD, d0 = (threadIdx.x % TD) * 4;
   f32x4_t early[kEarly];
 #pragma unroll
@@ -854,7 +854,11 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-bool attn_fits(const AttnArgs& a) { return (most_keys(a) + 31) / 32 * a.B < 0x7FFFFFFF; }
+bool attn_fits(const AttnArgs& a) {
+  const AttnLayout L = attn_layout(a.Hq / a.Hkv * a.Q, a.Hkv, a.D, a.cache_e4m3);
+  // tiles are numbered in 31 bits, a launch's work-items in 32
+  return (most_keys(a) + TK - 1) / TK * a.B < 0x7FFFFFFF && a.B * L.NHV <= 1 << 22;
+}
 
 size_t attn_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv, int64_t D) {
   if (B == 0 || Q == 0) return 0;

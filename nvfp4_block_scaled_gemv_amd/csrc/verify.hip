@@ -11,7 +11,7 @@
 // few dozen calls.
 //
 // Bound: the one row of p and one of q that the draw reads; the other rows
-// give one number each. Two launches: k_verify_sums, a workgroup per 2048
+// give one number each. Two launches: k_verify_sums, a workgroup per 1024
 // values of the row, finds the row (every workgroup for itself: a gather of Q
 // numbers) and sums its piece; k_verify_draw, a workgroup per sequence, finds
 // the piece that holds the border, then the token in it.
@@ -22,17 +22,20 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kPiece = 2048;     // values per workgroup of the sums
+constexpr int kPiece = 1024;     // values per workgroup of the sums
 constexpr int kPer = kPiece / 256;
 
-// The number of kept drafts; every thread of the wavefront gets it. Q <= 64.
+// The drafts of a sequence that are real.
+__device__ __forceinline__ int drafts_of(const VerifyArgs& a, int b) {
+  const int Q = (int)a.Q;
+  if (!a.n_draft) return Q;
+  const int n = a.n_draft[b];
+  return n < 0 ? 0 : n < Q ? n : Q;
+}
+// The number of kept drafts; every thread of the wavefront gets it. Q < 64.
 __device__ __forceinline__ int kept(const VerifyArgs& a, int b, int& nd) {
   const int lane = threadIdx.x & 63, Q = (int)a.Q;
-  nd = Q;
-  if (a.n_draft) {
-    const int n = a.n_draft[b];
-    nd = n < 0 ? 0 : n < Q ? n : Q;
-  }
+  nd = drafts_of(a, b);
   bool ok = false;
   if (lane < nd) {
     const int d = a.draft[(int64_t)b * Q + lane];
@@ -60,12 +63,28 @@ __device__ __forceinline__ Row row_of(const VerifyArgs& a, int b, int n, int nd)
   r.cut = n < nd && !a.q ? a.draft[(int64_t)b * a.Q + n] : -1;
   return r;
 }
-__device__ __forceinline__ double weight(const Row& r, int64_t v, double p) {
-  if (r.q) {
-    const double d = p - (double)r.q[v];
-    return d > 0.0 ? d : 0.0;
+__device__ __forceinline__ double weight(const Row& r, int64_t v, float p, float q) {
+  const double d = (double)p - (double)q;
+  return r.q ? (d > 0.0 ? d : 0.0) : v == r.cut ? 0.0 : (double)p;
+}
+// kPer values of p and q at first, first + step, ..; past the row its last one
+// (their weight is left out): no branch between the loads.
+__device__ __forceinline__ void load_row(const Row& r, int64_t first, int step, int64_t V,
+                                         float (&p)[kPer], float (&q)[kPer]) {
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int64_t v = first + i * step;
+    p[i] = r.p[v < V ? v : V - 1];
   }
-  return v == r.cut ? 0.0 : p;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) q[i] = 0.0f;
+  if (r.q) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int64_t v = first + i * step;
+      q[i] = r.q[v < V ? v : V - 1];
+    }
+  }
 }
 
 __device__ __forceinline__ double wave_sum_f64(double v) {
@@ -86,15 +105,14 @@ __global__ __launch_bounds__(256) void k_verify_sums(const VerifyArgs a, int pie
     if (j == 0) a.accepted[b] = n;
   }
   const int64_t v0 = (int64_t)piece * kPiece;
+  float p[kPer], q[kPer];
+  load_row(r, v0 + threadIdx.x, 256, a.V, p, q);
   double sr = 0.0, sp = 0.0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     const int64_t v = v0 + i * 256 + threadIdx.x;
-    if (v < a.V) {
-      const double p = r.p[v];
-      sr += weight(r, v, p);
-      sp += p;
-    }
+    sr += v < a.V ? weight(r, v, p[i], q[i]) : 0.0;
+    sp += v < a.V ? (double)p[i] : 0.0;
   }
   sr = wave_sum_f64(sr);
   sp = wave_sum_f64(sp);
@@ -110,117 +128,117 @@ __global__ __launch_bounds__(256) void k_verify_sums(const VerifyArgs a, int pie
   }
 }
 
-// Inclusive sums over the 256 threads; total: of all.
-__device__ __forceinline__ double block_scan(double v, double* lds, double& total) {
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+// Inclusive sums over the 64 lanes of a wavefront.
+__device__ __forceinline__ double wave_scan(double v) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
     const double o = __shfl_up(v, off, 64);
     if (lane >= off) v += o;
   }
-  __syncthreads();   // the last use of lds is over
-  if (lane == 63) lds[wv] = v;
-  __syncthreads();
-  double base = 0.0;
-  for (int w = 0; w < wv; ++w) base += lds[w];
-  total = ((lds[0] + lds[1]) + lds[2]) + lds[3];
-  return v + base;
+  return v;
 }
-// The lowest index that any thread offers (INT_MAX: none).
-__device__ __forceinline__ int block_min(int v, int* lds) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    const int o = __shfl_xor(v, off, 64);
-    v = o < v ? o : v;
-  }
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  int m = lds[0];
-  for (int w = 1; w < 4; ++w) m = lds[w] < m ? lds[w] : m;
-  return m;
+__device__ __forceinline__ double lane_f64(double v, int lane) {
+  const int64_t u = __builtin_bit_cast(int64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)u, lane);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(u >> 32), lane);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
+// The first index i below n with sum_{j <= i} x(j) > target, and the sum
+// before it; n if there is none. By one wavefront: a run of `per` numbers per
+// lane. total: of all (target_of(total) is the target).
+template <typename X, typename T>
+__device__ __forceinline__ int first_past(int n, X x, T target_of, double& before, double& total) {
+  const int lane = threadIdx.x & 63;
+  const int per = (n + 63) / 64, i0 = lane * per;
+  const int i1 = i0 + per < n ? i0 + per : n;
+  double mine = 0.0;
+  for (int i = i0; i < i1; ++i) mine += x(i);
+  const double incl = wave_scan(mine);
+  total = lane_f64(incl, 63);
+  const double target = target_of(total);
+  const uint64_t past = __ballot(incl > target);
+  before = 0.0;
+  if (!past) return n;
+  const int l = __builtin_ctzll(past);
+  // the lane's own run; a border that a rounding moved stays on its last
+  double run = incl - mine, at = run;
+  int found = i1 - 1;
+  for (int i = i0; i < i1; ++i) {
+    at = run;
+    run += x(i);
+    if (run > target) {
+      found = i;
+      break;
+    }
+  }
+  before = lane_f64(at, l);
+  return __builtin_amdgcn_readlane(found, l);
+}
+
+// Every wavefront finds the piece for itself (no barrier); the four of them
+// then share its values.
 __global__ __launch_bounds__(256) void k_verify_draw(const VerifyArgs a, int pieces) {
   __shared__ double lds[4];
-  __shared__ int ldsi[4];
-  __shared__ double lds_before;
-  const int b = blockIdx.x;
-  int nd;
-  const int n = kept(a, b, nd);
+  __shared__ int ldsi[2][4];
+  const int b = blockIdx.x, lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int n = a.accepted[b];   // by k_verify_sums
+  const int nd = drafts_of(a, b);
   Row r = row_of(a, b, n, nd);
+  const double u = a.u_sample[b];
   const double* sums = (const double*)a.workspace + (int64_t)b * pieces * 2;
-  // totals of the weights and of p: every thread a run of pieces
-  const int per = (pieces + 255) / 256;
-  const int i0 = threadIdx.x * per;
-  double mine = 0.0, mine_p = 0.0;
-  for (int i = i0; i < i0 + per && i < pieces; ++i) {
-    mine += sums[2 * i];
-    mine_p += sums[2 * i + 1];
-  }
-  double total, total_p;
-  double incl = block_scan(mine, lds, total);
-  const double incl_p = block_scan(mine_p, lds, total_p);
-  int which = 0;
+  double target = 0.0, before, total;
+  auto target_of = [&](double sum) { return target = u * sum; };
+  int piece = first_past(pieces, [&](int i) { return sums[2 * i]; }, target_of, before, total);
   if (!(total > 0.0)) {   // p <= q everywhere: draw from p
-    which = 1;
     r.q = nullptr;
     r.cut = -1;
-    incl = incl_p;
-    mine = mine_p;
-    total = total_p;
+    piece = first_past(pieces, [&](int i) { return sums[2 * i + 1]; }, target_of, before, total);
   }
-  const double target = (double)a.u_sample[b] * total;
-  // the piece: the first whose inclusive sum passes the target
-  int found = 0x7FFFFFFF;
-  double before = incl - mine;
-  if (incl > target) {
-    double run = before;
-    for (int i = i0; i < i0 + per && i < pieces; ++i) {
-      const double next = run + sums[2 * i + which];
-      if (next > target) {
-        found = i;
-        before = run;
-        break;
-      }
-      run = next;
-    }
-    if (found == 0x7FFFFFFF) {   // a rounding apart from the scan's own sum
-      const int last = i0 + per < pieces ? i0 + per : pieces;
-      found = last - 1;
-      before = run - sums[2 * found + which];
-    }
-  }
-  const int piece = block_min(found, ldsi);
-  if (piece == 0x7FFFFFFF) {   // nothing passes: u >= 1, or no probability at all
-    if (threadIdx.x == 0) a.tokens[(int64_t)b * (a.Q + 1) + n] = (int)a.V - 1;
+  int32_t* const out = a.tokens + (int64_t)b * (a.Q + 1) + n;
+  if (piece >= pieces) {   // nothing passes: u >= 1, or no probability at all
+    if (threadIdx.x == 0) *out = (int)a.V - 1;
     return;
   }
-  if (found == piece) lds_before = before;
-  __syncthreads();
-  before = lds_before;
-  // the token: 8 consecutive values per thread
+  // 8 consecutive values per thread
   const int64_t v0 = (int64_t)piece * kPiece + threadIdx.x * kPer;
+  float p[kPer], q[kPer];
+  load_row(r, v0, 1, a.V, p, q);
   double w[kPer], sum = 0.0;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    w[i] = v0 + i < a.V ? weight(r, v0 + i, r.p[v0 + i]) : 0.0;
+    w[i] = v0 + i < a.V ? weight(r, v0 + i, p[i], q[i]) : 0.0;
     sum += w[i];
   }
-  double all;
-  const double upto = block_scan(sum, lds, all) + before;
-  int token = 0x7FFFFFFF, last = -1;
-  double run = upto - sum;
+  const double incl = wave_scan(sum);
+  if (lane == 63) lds[wv] = incl;
+  __syncthreads();
+  double run = before + (incl - sum);
+  for (int k = 0; k < wv; ++k) run += lds[k];
+  int token = 0x7FFFFFFF, last = -1;   // the first past the target, the last with a weight
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     run += w[i];
     if (w[i] > 0.0) last = (int)(v0 + i);
     if (token == 0x7FFFFFFF && run > target && w[i] > 0.0) token = (int)(v0 + i);
   }
-  const int pick = block_min(token, ldsi);
-  const int end = -block_min(-last, ldsi);   // the piece's last value with a weight
-  if (threadIdx.x == 0)
-    a.tokens[(int64_t)b * (a.Q + 1) + n] = pick != 0x7FFFFFFF ? pick : end >= 0 ? end : (int)a.V - 1;
+  // values rise with the lane: the first lane that has one, the last that does
+  const uint64_t hit = __ballot(token != 0x7FFFFFFF), any = __ballot(last >= 0);
+  if (lane == 0) {
+    ldsi[0][wv] = -1;
+    ldsi[1][wv] = -1;
+  }
+  if (hit && lane == __builtin_ctzll(hit)) ldsi[0][wv] = token;
+  if (any && lane == 63 - __builtin_clzll(any)) ldsi[1][wv] = last;
+  __syncthreads();
+  if (threadIdx.x) return;
+  int pick = -1, end = (int)a.V - 1;
+  for (int k = 0; k < 4; ++k) {
+    if (pick < 0) pick = ldsi[0][k];
+    if (ldsi[1][k] >= 0) end = ldsi[1][k];
+  }
+  *out = pick >= 0 ? pick : end;
 }
 
 int64_t pieces_of(int64_t V) { return (V + kPiece - 1) / kPiece; }

@@ -158,6 +158,7 @@ def test_cache_checks(L):
     assert both(cache(v=None)) == ERR_NULL
     assert both(cache(v=A[8])) == ERR_NULL                # k and v the same array
     assert both(cache(t=E4M3, ks=A[10])) == ERR_NULL
+    assert both(cache(t=E4M3, ks=A[10], nb=0)) == ERR_NULL   # read also without a page
     assert both(cache(k=A[8] + 8)) == ERR_ALIGN
     assert both(cache(t=E4M3, ks=A[10] + 2, vs=A[11])) == ERR_ALIGN
 
@@ -188,6 +189,8 @@ def test_paged_attention_checks(L):
     assert attn(L, window=1 << 31) == ERR_UNSUPPORTED
     # more steps of 128 keys than 31 bits: 4096 sequences of 2^31 keys
     assert attn(L, B=4096, width=0x7FFFFFFF) == ERR_UNSUPPORTED
+    # more workgroups than a launch holds: 4096 sequences x 4096 row tiles
+    assert attn(L, B=4096, Q=64, Hq=1024, c=cache(heads=1, D=256)) == ERR_UNSUPPORTED
     assert attn(L, B=0, wb=0) == OK
     assert attn(L, Q=0, wb=0) == OK
     assert attn(L, Hq=0, wb=0) == OK
