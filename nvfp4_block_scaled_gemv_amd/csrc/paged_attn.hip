@@ -766,9 +766,11 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnS
   store8(a.out + ((int64_t)(b * a.Q + t) * a.Hq + h * sh.G + (rr - t * sh.G)) * D + d, out);
 }
 
-// Row tiles of 16 in one pass (heads of 256 keep one: their registers are
-// full); a head with more rows is read again for the others.
-int row_tiles(int64_t rows, int64_t D) { return rows <= 16 || D == 256 ? 1 : 2; }
+// Row tiles of 16 in one pass; a head with more rows is read again for the
+// others. Heads of 256 take two only where pages hold whole runs of 16 keys
+// (pg): 8 sequences of 20000 keys, 32 rows, 220 -> 170 us; without, one offset
+// per lane and key spills registers (40 rows, pages of 20: 108 -> 163 us).
+int row_tiles(int64_t rows, int64_t D, bool pg) { return rows <= 16 || (D == 256 && !pg) ? 1 : 2; }
 
 // The most runs per head (all heads' together fill the SIMDs), and where their
 // records lie in the workspace.
@@ -776,9 +778,9 @@ struct AttnLayout {
   size_t ml, o, total;
   int RT, slot_rows, NHV, groups;
 };
-AttnLayout attn_layout(int64_t rows, int64_t Hkv, int64_t D, bool e4m3) {
+AttnLayout attn_layout(int64_t rows, int64_t Hkv, int64_t D, bool e4m3, bool pg) {
   AttnLayout L;
-  L.RT = row_tiles(rows, D);
+  L.RT = row_tiles(rows, D, pg);
   L.NHV = (int)(Hkv * ((rows + L.RT * 16 - 1) / (L.RT * 16)));
   L.slot_rows = (int)(rows < L.RT * 16 ? rows : L.RT * 16);
   L.groups = kCus * 4 * waves_per_simd(L.RT, (int)D, e4m3) / L.NHV;
@@ -835,18 +837,17 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
   AttnShape sh;
   sh.G = (int)(a.Hq / a.Hkv);
   sh.rows = sh.G * (int)a.Q;
-  const AttnLayout L = attn_layout(sh.rows, a.Hkv, D, FP8);
+  const bool pg = a.page % 16 == 0;
+  const AttnLayout L = attn_layout(sh.rows, a.Hkv, D, FP8, pg);
   sh.NHV = L.NHV;
   sh.cap = capacity(a);
   sh.page_shift = (a.page & (a.page - 1)) == 0 ? __builtin_ctzll((uint64_t)a.page) : -1;
   sh.slot_rows = L.slot_rows;
   sh.ml = (float*)((char*)a.workspace + L.ml);
   sh.o = (float*)((char*)a.workspace + L.o);
-  const bool pg = a.page % 16 == 0;
-  if constexpr (D != 256) {
-    if (L.RT == 2)
-      return pg ? launch_rt<D, FP8, 2, true>(a, sh, L, stream)
-                : launch_rt<D, FP8, 2, false>(a, sh, L, stream);
+  if (L.RT == 2) {
+    if (pg) return launch_rt<D, FP8, 2, true>(a, sh, L, stream);
+    if constexpr (D < 256) return launch_rt<D, FP8, 2, false>(a, sh, L, stream);
   }
   return pg ? launch_rt<D, FP8, 1, true>(a, sh, L, stream)
             : launch_rt<D, FP8, 1, false>(a, sh, L, stream);
@@ -855,17 +856,20 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
 }  // namespace
 
 bool attn_fits(const AttnArgs& a) {
-  const AttnLayout L = attn_layout(a.Hq / a.Hkv * a.Q, a.Hkv, a.D, a.cache_e4m3);
+  const AttnLayout L = attn_layout(a.Hq / a.Hkv * a.Q, a.Hkv, a.D, a.cache_e4m3, a.page % 16 == 0);
   // tiles are numbered in 31 bits, a launch's work-items in 32
   return (most_keys(a) + TK - 1) / TK * a.B < 0x7FFFFFFF && a.B * L.NHV <= 1 << 22;
 }
 
 size_t attn_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv, int64_t D) {
   if (B == 0 || Q == 0) return 0;
-  // the call's cache type is not known here: the larger of the two
-  const size_t n = attn_layout(Hq / Hkv * Q, Hkv, D, false).total;
-  const size_t m = attn_layout(Hq / Hkv * Q, Hkv, D, true).total;
-  return n > m ? n : m;
+  // the call's cache type and page are not known here: the largest of all
+  size_t most = 0;
+  for (int i = 0; i < 4; ++i) {
+    const size_t n = attn_layout(Hq / Hkv * Q, Hkv, D, i & 1, i & 2).total;
+    most = n > most ? n : most;
+  }
+  return most;
 }
 
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream) {

@@ -91,6 +91,10 @@ CASES = [
     ([97, 200], 8, 8, 1, 128, 7, BF16, 0, "nhd"),        # 64 rows: two tiles of 32
     ([150], 5, 16, 1, 256, 48, BF16, 0, "nhd"),          # 80 rows of a 256 head
     ([400, 90, 1], 1, 64, 1, 64, 16, E4M3, 33, "nhd"),   # 64 heads on one
+    ([150, 1300], 5, 16, 2, 256, 20, BF16, 0, "nhd"),    # 40 rows of a 256 head, odd pages
+    ([150, 1300], 5, 16, 2, 256, 16, E4M3, 90, "hnd"),
+    ([700, 20], 3, 32, 2, 128, 3, E4M3, 0, "nhd"),       # 48 rows, one key of three to a page
+    ([1025, 513, 512], 1, 8, 8, 128, 16, BF16, 0, "hnd"),
     ([63] * 70, 1, 2, 1, 64, 16, BF16, 0, "nhd"),        # more sequences than lanes
     ([1, 2, 3, 4, 5, 6, 7, 8] * 17, 2, 4, 2, 64, 16, BF16, 0, "nhd"),
     ([2049], 64, 1, 1, 64, 128, BF16, 500, "nhd"),
