@@ -11,8 +11,10 @@
 // one store for a token. The row stays in registers between the sum of
 // squares and the scaling, so every byte moves once: W wavefronts hold one
 // row, VPT groups of 8 elements per lane, and all loads of a lane are issued
-// before the first use. Rows of at most 512 elements take one wavefront each,
-// four rows to a workgroup, and no LDS.
+// before the first use. Rows of at most 512 elements take one wavefront (of at
+// most 128 a quarter of one) and no LDS. Measured: one token of 7168, bf16 with
+// residual, 2.2 us; 2048 rows of 7168 to E4M3 with an fp32 residual 34 us, 162 MB at the
+// rate of a copy.
 #include "elems.h"
 #include "internal.h"
 
@@ -31,46 +33,65 @@ struct Residual {
 template <>
 struct Residual<None> {};
 
-// Sum (MAX: largest value) over the W wavefronts of a row; every thread gets
-// it. Fixed order. The two uses in a kernel take different LDS words, so one
-// barrier each is enough.
+// Sum (MAX: largest value) over a row's threads; each of them gets it. Fixed
+// order. lpr 16: the row is a DPP row; otherwise W wavefronts. The two uses in
+// a kernel take different LDS words, so one barrier each is enough.
 template <bool MAX>
-__device__ __forceinline__ float row_reduce(float v, int W, float* lds) {
-  if (MAX) {
-    v = fmaxf(v, dpp_f32<0xB1>(v));
-    v = fmaxf(v, dpp_f32<0x4E>(v));
-    v = fmaxf(v, dpp_f32<0x141>(v));
-    v = fmaxf(v, dpp_f32<0x140>(v));
-    float r[4];
+__device__ __forceinline__ float row_reduce(float v, int lpr, int W, float* lds) {
+  auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : a + b; };
+  v = join(v, dpp_f32<0xB1>(v));    // quad_perm [1,0,3,2]
+  v = join(v, dpp_f32<0x4E>(v));    // quad_perm [2,3,0,1]
+  v = join(v, dpp_f32<0x141>(v));   // row_half_mirror
+  v = join(v, dpp_f32<0x140>(v));   // row_mirror
+  if (lpr == 16) return v;
+  float r[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      r[i] = __builtin_bit_cast(float,
-                                __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 16 * i));
-    v = fmaxf(fmaxf(r[0], r[1]), fmaxf(r[2], r[3]));
-  } else {
-    v = wave_sum(v);
-  }
+  for (int i = 0; i < 4; ++i)
+    r[i] = __builtin_bit_cast(float,
+                              __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 16 * i));
+  v = join(join(r[0], r[1]), join(r[2], r[3]));
   if (W == 1) return v;
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
   v = lds[0];
-  for (int w = 1; w < W; ++w) v = MAX ? fmaxf(v, lds[w]) : v + lds[w];
+  for (int w = 1; w < W; ++w) v = join(v, lds[w]);
   return v;
+}
+
+// v[i] / d for 8 numbers: with r = 1 / d correctly rounded, q = v r is within an
+// ulp and a half, and q + (v - q d) r rounds to the quotient (of 5e7 quotients,
+// divisors next to powers of two among them, none differs from the division's;
+// two fused steps in place of a division each: E4M3 rows of 7168 fp32 values
+// were bound by the divisions, 86.6 us for 8192 of them). The division itself where d or
+// the largest |v[i]|, top, could take r, q or the remainder out of the normal
+// numbers (a saturated block scale leaves quotients as large as fp32 holds).
+__device__ __forceinline__ void divide8(float (&v)[8], float d, float top) {
+  if (d >= 0x1p-96f && d <= 0x1p96f && top <= d * 0x1p20f) {
+    const float r = 1.0f / d;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float q = v[e] * r;
+      v[e] = fmaf(fmaf(-q, d, v[e]), r, q);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = v[e] / d;
+  }
 }
 
 template <typename TX, typename TR, int OUT, int VPT>
 __global__ __launch_bounds__(1024) void k_add_rmsnorm(
     const TX* __restrict__ x, const TR* residual, TR* residual_out,   // may be one array
-    const uint16_t* __restrict__ weight, float eps, int64_t M, int H, int W, int group,
+    const uint16_t* __restrict__ weight, float eps, int64_t M, int H, int lpr, int W, int group,
     const float* __restrict__ gscale, void* __restrict__ out, void* __restrict__ out_scales) {
   constexpr bool kRes = !__is_same(TR, None);
   __shared__ float lds[32];
-  // W == 1: one row per wavefront; otherwise one row per workgroup
-  const int64_t row =
-      W == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 6) + (threadIdx.x >> 6) : (int64_t)blockIdx.x;
-  if (row >= M) return;   // whole wavefronts, and only where no barrier follows
-  const int lane = W == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
-  const int lanes = W * 64;
+  // W == 1: 64 / lpr rows per wavefront; otherwise one row per workgroup
+  const int64_t row = W == 1 ? ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / lpr
+                             : (int64_t)blockIdx.x;
+  if (row >= M) return;   // whole DPP rows or wavefronts, and no barrier follows
+  const int lane = W == 1 ? (int)threadIdx.x & (lpr - 1) : (int)threadIdx.x;
+  const int lanes = W == 1 ? lpr : W * 64;
   const int64_t at = row * H;
   Raw8<TX> rx[VPT];
   Residual<TR> rr[VPT];
@@ -105,7 +126,7 @@ __global__ __launch_bounds__(1024) void k_add_rmsnorm(
       for (int e = 0; e < 8; ++e) s[v][e] = 0.0f;
     }
   }
-  sq = row_reduce<false>(sq, W, lds);
+  sq = row_reduce<false>(sq, lpr, W, lds);
   const float rstd = 1.0f / sqrtf(sq / (float)H + eps);
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
@@ -138,7 +159,7 @@ __global__ __launch_bounds__(1024) void k_add_rmsnorm(
     // a group of 32, 64 or 128 elements is 4, 8 or 16 lanes of one DPP row;
     // H is a multiple of the group, so its lanes are all inside the row
     if (group == 0) {
-      all = row_reduce<true>(all, W, lds + 16);
+      all = row_reduce<true>(all, lpr, W, lds + 16);
 #pragma unroll
       for (int v = 0; v < VPT; ++v) am[v] = all;
     } else {
@@ -157,10 +178,8 @@ __global__ __launch_bounds__(1024) void k_add_rmsnorm(
       const int i = (v * lanes + lane) * 8;
       if (i < H) {
         const float scale = am[v] > 0.0f ? am[v] / 448.0f : 1.0f;
-        float q[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q[e] = s[v][e] / scale;
-        store8((uint8_t*)out + at + i, q);
+        divide8(s[v], scale, am[v]);
+        store8((uint8_t*)out + at + i, s[v]);
         if (i % gsize == 0) sc[i / gsize] = scale;
       }
     }
@@ -179,9 +198,9 @@ __global__ __launch_bounds__(1024) void k_add_rmsnorm(
     const float sv = e4m3_to_f32<0>(code);
     uint32_t word = 0u;
     if (sv != 0.0f) {
-      const float dn = sv * g;
+      divide8(s[v], sv * g, ab);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) word |= e2m1_encode(s[v][e] / dn) << (4 * e);
+      for (int e = 0; e < 8; ++e) word |= e2m1_encode(s[v][e]) << (4 * e);
     }
     if (i < H) {
       reinterpret_cast<uint32_t*>(out)[(at + i) >> 3] = word;
@@ -192,19 +211,27 @@ __global__ __launch_bounds__(1024) void k_add_rmsnorm(
 
 template <typename TX, typename TR, int OUT, int VPT>
 hipError_t launch_v(const NormArgs& a, int W, hipStream_t stream) {
-  const int rows = W == 1 ? 4 : 1;   // rows per workgroup
+  // rows of at most 128: 16 lanes each (163840 rows of 128, bf16 with a
+  // residual: 25.5 us, 37.6 with a wavefront each)
+  const int lpr = a.H <= 128 ? 16 : 64;
+  const int rows = W == 1 ? 256 / lpr : 1;   // rows per workgroup
   const int64_t grid = (a.M + rows - 1) / rows;
-  hipLaunchKernelGGL((k_add_rmsnorm<TX, TR, OUT, VPT>), dim3((uint32_t)grid), dim3(64 * W * rows),
-                     0, stream, (const TX*)a.x, (const TR*)a.residual, (TR*)a.residual_out,
-                     a.weight, a.eps, a.M, (int)a.H, W, a.group, a.gscale, a.out, a.out_scales);
+  hipLaunchKernelGGL((k_add_rmsnorm<TX, TR, OUT, VPT>), dim3((uint32_t)grid),
+                     dim3(W == 1 ? 256 : 64 * W), 0, stream, (const TX*)a.x, (const TR*)a.residual,
+                     (TR*)a.residual_out, a.weight, a.eps, a.M, (int)a.H, lpr, W, a.group,
+                     a.gscale, a.out, a.out_scales);
   return hipGetLastError();
 }
 
 template <typename TX, typename TR, int OUT>
 hipError_t launch_o(const NormArgs& a, hipStream_t stream) {
-  // groups of 8 per lane: one while the row fits 1024 threads that way
-  const int64_t vecs = a.H / 8;
-  const int VPT = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : 4;
+  // Groups of 8 per lane: one while the row fits 1024 threads that way, which
+  // is the shortest way through few rows (512 rows of 7168, NVFP4: 7.0 us, 9.8
+  // with four). From 1024 rows on fewer threads per row, so that more rows are
+  // in flight where one reduces: 8192 rows of 7168 fp32 to E4M3 71.4 -> 46.7 us,
+  // to bf16 64.0 -> 58.4; 16384 rows of 4096 to NVFP4 77.6 -> 65.6.
+  const int64_t vecs = a.H / 8, one = a.M >= 1024 ? 256 : 1024;
+  const int VPT = vecs <= one ? 1 : vecs <= 2 * one ? 2 : 4;
   const int W = (int)((vecs + 64 * VPT - 1) / (64 * VPT));
   return VPT == 1   ? launch_v<TX, TR, OUT, 1>(a, W, stream)
          : VPT == 2 ? launch_v<TX, TR, OUT, 2>(a, W, stream)

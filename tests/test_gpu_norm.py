@@ -166,11 +166,45 @@ def test_empty_calls():
     assert y.shape == (0, 64)
 
 
-def test_many_rows():
-    """More rows than a grid of one round, and the last workgroup part empty."""
-    M, H = 70001, 64
+@pytest.mark.parametrize("M,H", [(70001, 64), (1024, 2056), (1025, 4104), (1500, 8192),
+                                 (1030, 16640)])
+def test_many_rows(M, H):
+    """More rows than a grid of one round, the last workgroup part empty, and
+    the shapes of 1024 rows and more."""
     x = torch.randn(M, H, device=DEV, generator=torch.Generator(DEV).manual_seed(3))
-    w = torch.ones(H, dtype=BF16, device=DEV)
+    w = (1 + 0.2 * torch.randn(H, device=DEV, generator=torch.Generator(DEV).manual_seed(4))).to(BF16)
     y, _ = nv.add_rmsnorm(x, w, EPS)
     yr, _ = rmsnorm(x, w, EPS)
     assert torch.all((y.double() - yr).abs() <= yr.abs() * (2.0 ** -8 + F32_STEPS) + 1e-37)
+    if H % 128 == 0:
+        y8, sc, _ = nv.add_rmsnorm_e4m3(x, w, EPS, group=128)
+        t = yr.view(M, -1, 128)
+        scale = t.abs().amax(-1, keepdim=True) / 448
+        tol = torch.maximum((t / scale).abs() * 2.0 ** -4,
+                            torch.tensor(2.0 ** -10, dtype=torch.float64, device=DEV))
+        q = y8.float().double().view(M, -1, 128)
+        assert torch.all((q - t / scale).abs() <= tol + (t / scale).abs() * 3 * F32_STEPS)
+        one, s1, _ = nv.add_rmsnorm_nvfp4(x, w, EPS, torch.full((1,), 0.0017, device=DEV))
+        few, s2, _ = nv.add_rmsnorm_nvfp4(x[:7].contiguous(), w, EPS,
+                                          torch.full((1,), 0.0017, device=DEV))
+        # fewer rows take another shape, whose sum may round the other way:
+        # a code in a thousand may lie on the other side of a border
+        assert float((one[:7] != few).float().mean()) < 1e-3
+        assert float((s1[:7] != s2).float().mean()) < 1e-3
+
+
+@pytest.mark.parametrize("M,H", [(1, 64), (3, 4096), (1100, 4096)])
+@pytest.mark.parametrize("big", [1e6, 1e30, 3e38, float("inf")])
+def test_nvfp4_saturates(M, H, big):
+    """Values far above what the static scale covers take the largest code,
+    whatever the quotient, infinite ones too."""
+    x = torch.ones(M, H, device=DEV)
+    x[:, 1::2] = -1
+    w = torch.ones(H, dtype=BF16, device=DEV)
+    w[16:32] = big
+    q, s, _ = nv.add_rmsnorm_nvfp4(x, w, EPS, torch.full((1,), 2.0 ** -9, device=DEV))
+    assert torch.all(s[:, 1] == 0x7E)
+    assert torch.all(q.view(torch.uint8)[:, 8:16] == 0xF7)
+    s1 = s[:, :1].clone()
+    assert torch.all(s[:, 2:] == s1) and torch.all(s[:, 0] == s1[:, 0])
+    assert torch.all(q.view(torch.uint8)[:, :8] == 0xF7)
