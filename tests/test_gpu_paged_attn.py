@@ -54,19 +54,19 @@ def run(q, table, lens, kc, vc, ks, vs, ct, scale=None, window=0):
 
 
 def check(got, q, k, v, table, lens, scale, window, ks, vs):
-    """The bound. A probability is rounded to bf16 (2^-8 of it at most, in the
-    product with V and not in the sum), the scores are off by the products'
+    """The bound. A probability enters the product with V as two bf16 (2^-16 of
+    it at most is lost, and not in the sum), the scores are off by the products'
     fp32 sums (D terms of at most |q||k|, 2^-24 each for D / 32 + 8 additions,
     taken as 2 D 2^-24 sum |q k|) and the output by half a bf16 step; sums over
     the keys in fp32 add 2^-24 per addition of the longest chain, taken as
     2^-14 in all. With a = sum_j p_j |v_j| the error is at most
-    a * (2^-8 + 2 * dscore + 2^-14) + |o| 2^-8."""
+    a * (2^-16 + 2 * dscore + 2^-14) + |o| 2^-8."""
     ref = attention(q, k, v, table, lens, scale, window, ks, vs)
     a = attention(q, k, v.double().abs(), table, lens, scale, window, ks, vs)
     D = q.shape[-1]
     size = q.double().norm(dim=-1).max() * (k.double() * ks).norm(dim=-1).max() * scale
     dscore = 2 * D * 2.0 ** -24 * float(size)
-    tol = a * (2.0 ** -8 + 2 * dscore + 2.0 ** -14) + ref.abs() * 2.0 ** -8 + 1e-30
+    tol = a * (2.0 ** -16 + 2 * dscore + 2.0 ** -14) + ref.abs() * 2.0 ** -8 + 1e-30
     err = (got - ref).abs()
     bad = ~(err <= tol)
     assert not bad.any(), (int(bad.sum()), float((err / tol).max()), torch.nonzero(bad)[0].tolist())
@@ -160,6 +160,26 @@ def test_what_no_token_sees_does_not_reach_it(page):
         got = run(q, table, ln, kc, vc, ks, vs, BF16, window=window)
         assert torch.equal(got[:Q - 1], clean[:Q - 1]) and torch.equal(got[Q:], clean[Q:])
         assert torch.isnan(got[Q - 1]).all() or bad == -float("inf")
+
+
+@pytest.mark.parametrize("D,Q,ct", [(64, 1, BF16), (128, 3, E4M3), (256, 2, BF16)])
+def test_values_that_are_not_finite_stay_in_their_sequence(D, Q, ct):
+    """A NaN value that every token of its sequence sees gives NaN in its
+    dimension, an infinite one infinity or NaN (its probability is the sum of
+    two bf16, the second of either sign or zero: inf + inf, inf - inf or
+    inf + 0 inf); other sequences and heads stay as they were."""
+    q, k, v, table, ln, kc, vc, ks, vs = build([1500, 700, 90], Q, 4, 2, D, 16, ct, seed=11)
+    clean = run(q, table, ln, kc, vc, ks, vs, ct)
+    for bad in (float("nan"),) if ct is E4M3 else (float("nan"), float("inf")):
+        v2 = v.clone()
+        v2.view(torch.uint8 if ct is E4M3 else torch.int16)[table[1, 20], 3, 1, 5] = \
+            torch.tensor([bad]).to(ct).view(torch.uint8 if ct is E4M3 else torch.int16)[0]
+        vc.copy_(v2)
+        got = run(q, table, ln, kc, vc, ks, vs, ct)
+        assert torch.equal(got[:Q], clean[:Q]) and torch.equal(got[2 * Q:], clean[2 * Q:])
+        assert torch.equal(got[Q:2 * Q, :2], clean[Q:2 * Q, :2])
+        hit = got[Q:2 * Q, 2:, 5]
+        assert torch.all(torch.isnan(hit) | ((hit == bad) if bad == bad else False))
 
 
 def test_pages_that_do_not_exist_hide_their_keys():

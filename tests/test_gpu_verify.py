@@ -96,6 +96,46 @@ def test_sparse_rows():
             assert int(tokens[0, 0]) == int(rt[0, 0]) and int(rt[0, 0]) in at
 
 
+@pytest.mark.parametrize("V,count", [(300, 64), (5000, 512), (151936, 4096)])
+def test_exact_borders(V, count):
+    """`count` equal weights of a power of two at random places: every sum is
+    exact, and u = i / count is the border itself, which belongs to the entry
+    after it."""
+    g = gen(V)
+    at = torch.randperm(V, generator=g)[:count].sort().values
+    p = torch.zeros(1, 1, V)
+    p[0, 0, at] = 1.0 / count
+    B = 128
+    i = torch.randint(0, count, (B,), generator=g)
+    below = torch.nextafter((i + 1).float() / count, torch.zeros(()))
+    none = torch.zeros(B, 0, dtype=torch.int32, device=DEV)
+    pg = p.to(DEV).expand(B, 1, V).contiguous()
+    for u in (i.float() / count, below):
+        tokens, acc = nv.verify_draft(pg, None, none, torch.zeros(B, 0, device=DEV), u.to(DEV))
+        assert torch.equal(tokens[:, 0].cpu().long(), at[i])
+
+
+def test_every_token_has_weight():
+    """u at the fp32 neighbours of the borders of rows that are mostly zeros:
+    whatever the rounding of a sum, an entry without weight is never drawn."""
+    V, B = 60000, 512
+    g = gen(12)
+    row = torch.zeros(V)
+    at = torch.randperm(V, generator=g)[:300].sort().values
+    row[at] = torch.rand(300, generator=g) ** 4
+    c = torch.cumsum(row.double(), 0)
+    u = (c[at] / c[-1]).float()[torch.randint(0, 299, (B,), generator=g)]
+    u[::3] = torch.nextafter(u[::3], torch.zeros(()))
+    none = torch.zeros(B, 0, dtype=torch.int32, device=DEV)
+    tokens, _ = nv.verify_draft(row.to(DEV).expand(B, 1, V).contiguous(), None, none,
+                                torch.zeros(B, 0, device=DEV), u.to(DEV))
+    t = tokens[:, 0].cpu().long()
+    assert torch.all(row[t] > 0)
+    # and it is the border's: the sums around it enclose the target
+    target = u.double() * c[-1]
+    assert torch.all((c[t] > target - 1e-9) & (c[t] - row[t].double() <= target + 1e-9))
+
+
 def test_nothing_to_draw_from():
     """Zeros, NaN and u = 1 give a token inside the vocabulary."""
     V = 2500
