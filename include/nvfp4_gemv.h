@@ -656,7 +656,7 @@ size_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, i
  *                entries past a sequence's last page are not used;
  *   seq_lens     int32[B], the new tokens included; more than max_blocks *
  *                page counts as that;
- *   scale        the scores' factor, usually 1 / sqrt(D);
+ *   scale        the scores' factor, finite, usually 1 / sqrt(D);
  *   B, Q         0 <= B <= NVFP4_ATTN_MAX_B, 0 <= Q <= NVFP4_ATTN_MAX_Q;
  *   Hq           a multiple of the cache's n_kv_heads, <= NVFP4_MAX_HEADS. B *
  *                n_kv_heads * (row tiles of 16 of the Hq / n_kv_heads * Q rows)

@@ -724,7 +724,7 @@ def add_rmsnorm_nvfp4_into(x, weight, eps, gscale, codes, scales, residual=None,
     *a, M, H = _norm_args(x, weight, residual, residual_out, gscale, codes, scales)
     if gscale.dtype is not torch.float32 or codes.dtype is not torch.uint8 \
             or scales.dtype is not torch.uint8 or codes.shape != (M, H // 2) \
-            or scales.shape != (M, H // 16):
+            or scales.shape != (M, H // 16) or gscale.numel() != 1:
         raise ValueError("gscale must be fp32 [1], codes u8 [M, H/2], scales u8 [M, H/16]")
     _check("nvfp4_add_rmsnorm_nvfp4", lib().nvfp4_add_rmsnorm_nvfp4(
         *a, eps, M, H, gscale.data_ptr(), codes.data_ptr(), scales.data_ptr(), _stream(x)))
@@ -757,7 +757,8 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale) -> KvCache:
     if ct == _E4M3:
         if k_scale is None or v_scale is None:
             raise ValueError("an e4m3 cache needs k_scale and v_scale")
-        if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
+        if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32 \
+                or k_scale.numel() != 1 or v_scale.numel() != 1:
             raise TypeError("k_scale and v_scale must be fp32 [1]")
         ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     else:
@@ -781,6 +782,8 @@ def rope_append_into(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cach
     x = k if q is None else q
     if x is None:
         raise ValueError("neither q nor k is given")
+    if (k is None) != (v is None) or (k is not None and (k_cache is None or v_cache is None)):
+        raise ValueError("k, v and the caches go together")
     _same_device(x.get_device(), q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache,
                  k_scale, v_scale)
     xt = _ACT_TYPES.get(x.dtype)

@@ -693,6 +693,8 @@ nvfp4_status nvfp4_paged_attention(const uint16_t* q, const nvfp4_kv_cache* cach
                 "%s: need B, Q, max_blocks, window >= 0 and Hq a multiple of the cache's heads "
                 "(B=%lld Q=%lld Hq=%lld Hkv=%lld)", fn, (long long)B, (long long)Q,
                 (long long)Hq, (long long)Hkv);
+  if (!(scale > -3.0e38f && scale < 3.0e38f))
+    return fail(NVFP4_ERR_SHAPE, "%s: scale must be finite", fn);
   if (!attn_sizes(B, Q, Hq, Hkv, D))
     return fail(NVFP4_ERR_UNSUPPORTED,
                 "%s: B=%lld (max %d), Q=%lld (max %d), Hq=%lld (max %d), D=%lld (64, 128 or 256)",

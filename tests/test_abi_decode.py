@@ -181,6 +181,8 @@ def test_paged_attention_checks(L):
     assert attn(L, Hq=3) == ERR_SHAPE                     # not a multiple of the heads
     assert attn(L, width=-1) == ERR_SHAPE
     assert attn(L, window=-1) == ERR_SHAPE
+    assert attn(L, scale=float("inf")) == ERR_SHAPE
+    assert attn(L, scale=float("nan")) == ERR_SHAPE
     assert attn(L, B=nv.ATTN_MAX_B + 1, wb=1 << 30) == ERR_UNSUPPORTED
     assert attn(L, Q=nv.ATTN_MAX_Q + 1, wb=1 << 30) == ERR_UNSUPPORTED
     assert attn(L, Hq=nv.MAX_HEADS + 2, wb=1 << 30) == ERR_UNSUPPORTED
@@ -275,3 +277,11 @@ def test_bindings_raise_without_device_tensors():
     with pytest.raises(ValueError):
         nv.verify_draft(torch.zeros(1, 2, 8), None, torch.zeros(1, 1, dtype=torch.int32),
                         torch.zeros(1, 1, dtype=f), torch.zeros(1, dtype=f))
+    with pytest.raises(ValueError, match="go together"):      # k without v, or without pages
+        nv.rope_append(None, torch.zeros(2, 1, 64), None, one, one, torch.ones(32), c, c.clone())
+    with pytest.raises(ValueError, match="go together"):
+        nv.rope_append(torch.zeros(2, 1, 64), None, torch.zeros(2, 1, 64), one, one,
+                       torch.ones(32), c, c.clone())
+    with pytest.raises(ValueError, match="go together"):
+        nv.rope_append(None, torch.zeros(2, 1, 64), torch.zeros(2, 1, 64), one, one,
+                       torch.ones(32), None, None)

@@ -247,3 +247,15 @@ def test_cache_past_4_gib():
     ln = torch.tensor([500], dtype=torch.int32)
     got = run(q, ids, ln, kc, vc, 1.0, 1.0, BF16)
     check(got, q, k, v, torch.arange(4, dtype=torch.int32)[None], ln, D ** -0.5, 0, 1.0, 1.0)
+
+
+def test_one_scale_for_a_cache():
+    """A scale for each head is refused (the first would count for all)."""
+    q, k, v, table, ln, kc, vc, ks, vs = build([40], 1, 4, 2, 64, 16, E4M3)
+    two, one = torch.ones(2, device=DEV), torch.ones(1, device=DEV)
+    for a, b in ((two, one), (one, two), (one.double(), one)):
+        with pytest.raises(TypeError):
+            nv.paged_attention(q.to(DEV), kc, vc, table.to(DEV), ln.to(DEV), k_scale=a, v_scale=b)
+    x = torch.ones(1, 64, device=DEV)
+    with pytest.raises(ValueError):
+        nv.add_rmsnorm_nvfp4(x, torch.ones(64, dtype=BF16, device=DEV), 1e-6, two)
