@@ -16,8 +16,8 @@
 // numbers) and sums its piece; k_verify_draw, a workgroup per sequence, finds
 // the piece that holds the border, then the token in it. A second launch costs
 // less than a workgroup that waits for the others' sums. Measured: one sequence
-// of 4 drafts, 151936 entries: 3.6 + 3.7 us, each the latency of two dependent
-// loads; 16 of them with draft probabilities, 19.4 MB: 7.4 + 4.8 us.
+// of 4 drafts, 151936 entries: 3.5 + 3.6 us, each the latency of two dependent
+// loads; 16 of them with draft probabilities, 19.4 MB: 6.4 + 4.3 us.
 #include "elems.h"
 #include "internal.h"
 
@@ -25,7 +25,7 @@ namespace nvfp4 {
 
 namespace {
 
-// Values per workgroup of the sums: 16 sequences 7.4 us, more with 2048 or 4096.
+// Values per workgroup of the sums: 16 sequences 6.4 us, more with 2048 or 4096.
 constexpr int kPiece = 1024;
 constexpr int kPer = kPiece / 256;
 
