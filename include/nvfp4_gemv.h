@@ -646,8 +646,8 @@ size_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, i
  * gives zeros. A key or value that a token does not see does not reach it,
  * whatever its bits are (NaN and infinities included). A NaN value gives NaN
  * for the tokens that see it, in its dimension or in all of them; an infinite
- * one may give NaN too. Scores, maxima and sums are fp32; the probabilities
- * enter the product with V as the sum of two bf16 (16 bits).
+ * one may give NaN too. Scores, maxima, sums and probabilities are fp32; the
+ * probabilities enter the product with V whole, as the sum of three bf16.
  *
  *   q            bf16[B * Q, Hq, D] (uint16 bits), 16-byte aligned;
  *   cache        bf16 or E4M3, D 64, 128 or 256;

@@ -248,6 +248,7 @@ struct AttnWave {
   static constexpr int KL = D * ES / 64;       // 16-byte loads of K per lane and 16 keys
   static constexpr int NO = PG ? NU : 1;
   static constexpr uint32_t kAll = 0xFFFFFFFFu;
+  static constexpr int kParts = 3;             // bf16 numbers that hold a probability
 
   const AttnArgs& a;
   const AttnShape& sh;
@@ -411,9 +412,14 @@ struct AttnWave {
       for (int rt = 0; rt < RT; ++rt) S[rt][u] *= c;
     }
   }
-  // The running maximum and sum, and P as the sum of two bf16: in one, its
-  // rounding (2^-9 of each weight) would be as large as the output's own.
-  __device__ __forceinline__ void softmax(const f32x4_t (&S)[RT][NU], u32x4_t (&pf)[RT][NP], u32x4_t (&pl)[RT][NP]) {
+  // The running maximum and sum, and P as the sum of three bf16, which hold all
+  // 24 bits of it: each takes the upper half of what the ones before it leave.
+  // Two would hold 16 bits, and where the values of a head cancel their
+  // rounding (2^-18 of each weight) would stand above the output's: of 8192
+  // outputs over 1277 keys 20 rounded the other way, 2 with three. The third
+  // takes a half more of these products: 5 tokens on 32773 keys 27.8 -> 28.3 us,
+  // 700 keys 6.2 -> 6.3, a short batch with two row tiles 16.3 -> 17.3.
+  __device__ __forceinline__ void softmax(const f32x4_t (&S)[RT][NU], u32x4_t (&pf)[kParts][RT][NP]) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       float mx = -INFINITY;
@@ -435,9 +441,13 @@ struct AttnWave {
         const float p0 = __builtin_amdgcn_exp2f(S[rt][e >> 1][(e & 1) * 2] - m_use);
         const float p1 = __builtin_amdgcn_exp2f(S[rt][e >> 1][(e & 1) * 2 + 1] - m_use);
         l[rt] += p0 + p1;
-        const uint32_t top = pack_bf16(p0, p1);
-        pf[rt][e >> 2][e & 3] = top;
-        pl[rt][e >> 2][e & 3] = pack_bf16(p0 - bf16_lo(top), p1 - bf16_hi(top));
+        uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          pf[i][rt][e >> 2][e & 3] = perm_hi(u0, u1);
+          u0 = __float_as_uint(__uint_as_float(u0) - bf16_hi(u0));   // exact
+          u1 = __float_as_uint(__uint_as_float(u1) - bf16_hi(u1));
+        }
       }
     }
   }
@@ -445,8 +455,8 @@ struct AttnWave {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, v),
                                                    __builtin_bit_cast(bf16x8_t, pf), acc, 0, 0, 0);
   }
-  // O += V^T P^T
-  __device__ __forceinline__ void values(const u32x4_t (&pf)[RT][NP], const u32x4_t (&pl)[RT][NP]) {
+  // O += V^T P^T, the smallest parts first
+  __device__ __forceinline__ void values(const u32x4_t (&pf)[kParts][RT][NP]) {
 #pragma unroll
     for (int d = 0; d < NV / 2; ++d) {
 #pragma unroll
@@ -459,12 +469,12 @@ struct AttnWave {
         const u32x4_t hi = {perm_hi(x[0], x[1]), perm_hi(x[2], x[3]), perm_hi(x[4], x[5]),
                             perm_hi(x[6], x[7])};
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          O[rt][2 * d] = product(lo, pl[rt][q], O[rt][2 * d]);
-          O[rt][2 * d + 1] = product(hi, pl[rt][q], O[rt][2 * d + 1]);
-          O[rt][2 * d] = product(lo, pf[rt][q], O[rt][2 * d]);
-          O[rt][2 * d + 1] = product(hi, pf[rt][q], O[rt][2 * d + 1]);
-        }
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int i = kParts - 1; i >= 0; --i) {
+            O[rt][2 * d] = product(lo, pf[i][rt][q], O[rt][2 * d]);
+            O[rt][2 * d + 1] = product(hi, pf[i][rt][q], O[rt][2 * d + 1]);
+          }
       }
     }
   }
@@ -517,7 +527,7 @@ struct AttnWave {
     for (;;) {
       const bool more = --count > 0;
       f32x4_t S[RT][NU];
-      u32x4_t pf[RT][NP], pl[RT][NP];
+      u32x4_t pf[kParts][RT][NP];
       scores(S);
       const uint32_t ok_now = ok;
       resolve();
@@ -545,12 +555,12 @@ struct AttnWave {
           }
         }
       }
-      softmax(S, pf, pl);
+      softmax(S, pf);
       if (!all) {
         drop(cur, ok_now, t0, t1);
         if (t1 > t0) settle(weightless);
       }
-      values(pf, pl);
+      values(pf);
       load_v(more);
       if (!more || nxt.b != cur.b) {
 #pragma unroll
