@@ -708,8 +708,11 @@ def add_rmsnorm_e4m3_into(x, weight, eps, y8, scales, residual=None, residual_ou
 
 
 def add_rmsnorm_e4m3(x, weight, eps, residual=None, group: int = 0):
-    """(y8, scales, residual_out)."""
+    """(y8, scales, residual_out); group 0 (a scale for each row), 32, 64 or
+    128, dividing H."""
     M, H = x.shape
+    if group not in (0, 32, 64, 128) or (group and H % group):
+        raise ValueError(f"group must be 0, 32, 64 or 128 and divide H = {H}, got {group}")
     y8 = torch.empty((M, H), dtype=torch.float8_e4m3fn, device=x.device)
     scales = torch.empty((M, H // group if group else 1), dtype=torch.float32, device=x.device)
     r = None if residual is None else torch.empty_like(residual)
