@@ -751,9 +751,10 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale) -> KvCache:
     ct = _CACHE_TYPES.get(k_cache.dtype)
     if ct is None or v_cache.dtype is not k_cache.dtype:
         raise TypeError("the caches must both be bf16 or float8_e4m3fn")
-    st = k_cache.stride()
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.stride() != st \
-            or st[3] != 1:
+    st, sv = k_cache.stride(), v_cache.stride()
+    # the stride of a dimension of one says nothing
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or st[3] != 1 \
+            or (sv != st and any(n > 1 and a != b for n, a, b in zip(k_cache.shape, st, sv))):
         raise ValueError("the caches must have one shape [blocks, page, heads, D] and the same "
                          "strides, the last one 1")
     nb, page, heads, D = k_cache.shape
@@ -766,7 +767,6 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale) -> KvCache:
         ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
     else:
         ks = vs = None
-    # the stride of a dimension of one says nothing
     return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, nb, page, heads, D,
                    st[0] if nb > 1 else D, st[1] if page > 1 else D, st[2] if heads > 1 else D,
                    ct)
