@@ -519,7 +519,7 @@ nvfp4_status nvfp4_add_rmsnorm(const void* x, int x_type, const void* residual,
  * nvfp4_add_rmsnorm_e4m3 -- nvfp4_add_rmsnorm with an 8-bit output: for every
  * run of `group` elements of a row (the whole row where group is 0)
  *
- *   scale = max|y| / 448  (1 where that is 0),  y8 = E4M3(y / scale)
+ *   scale = max|y| / 448  (1 where that is 0 in fp32),  y8 = E4M3(y / scale)
  *
  * with y in fp32 (IEEE divisions, round to nearest even, saturating).
  *

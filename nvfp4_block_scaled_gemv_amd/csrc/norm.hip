@@ -177,7 +177,8 @@ __global__ __launch_bounds__(1024) void k_add_rmsnorm(
     for (int v = 0; v < VPT; ++v) {
       const int i = (v * lanes + lane) * 8;
       if (i < H) {
-        const float scale = am[v] > 0.0f ? am[v] / 448.0f : 1.0f;
+        float scale = am[v] / 448.0f;
+        if (!(scale > 0.0f)) scale = 1.0f;   // zeros, or too small for a scale
         divide8(s[v], scale, am[v]);
         store8((uint8_t*)out + at + i, s[v]);
         if (i % gsize == 0) sc[i / gsize] = scale;
