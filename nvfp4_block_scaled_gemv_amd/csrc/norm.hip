@@ -15,6 +15,7 @@
 // most 128 a quarter of one) and no LDS. Measured: one token of 7168, bf16 with
 // residual, 2.2 us; 2048 rows of 7168 to E4M3 with an fp32 residual 34 us, 162 MB at the
 // rate of a copy.
+#include "divide.h"
 #include "elems.h"
 #include "internal.h"
 
@@ -58,21 +59,16 @@ __device__ __forceinline__ float row_reduce(float v, int lpr, int W, float* lds)
   return v;
 }
 
-// v[i] / d for 8 numbers: with r = 1 / d correctly rounded, q = v r is within an
-// ulp and a half, and q + (v - q d) r rounds to the quotient (of 5e7 quotients,
-// divisors next to powers of two among them, none differs from the division's;
-// two fused steps in place of a division each: E4M3 rows of 7168 fp32 values
-// were bound by the divisions, 86.6 us for 8192 of them). The division itself where d or
-// the largest |v[i]|, top, could take r, q or the remainder out of the normal
-// numbers (a saturated block scale leaves quotients as large as fp32 holds).
+// v[i] / d for 8 numbers, two fused steps in place of a division each: E4M3 rows
+// of 7168 fp32 values were bound by the divisions, 86.6 us for 8192 of them.
+// The division itself where d or the largest |v[i]|, top, could take a step out
+// of the normal numbers (a saturated block scale leaves quotients as large as
+// fp32 holds).
 __device__ __forceinline__ void divide8(float (&v)[8], float d, float top) {
-  if (d >= 0x1p-96f && d <= 0x1p96f && top <= d * 0x1p20f) {
+  if (divides_fast(d, top)) {
     const float r = 1.0f / d;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float q = v[e] * r;
-      v[e] = fmaf(fmaf(-q, d, v[e]), r, q);
-    }
+    for (int e = 0; e < 8; ++e) v[e] = quotient(v[e], d, r);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = v[e] / d;
