@@ -53,9 +53,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;
 // s_waitcnt vmcnt(0), no other counter.
 constexpr int kVmcnt0 = 0x0F70;
-// Runs of one head at most.
-constexpr int kMaxRuns = kCus * 4 * 2;
-
 constexpr int TK = 32;   // keys per tile
 // Wavefronts per SIMD of the split form. Few long streams read memory best:
 // heads of 256 bytes and more keep 16 KB and more in flight per wavefront with
@@ -63,6 +60,10 @@ constexpr int TK = 32;   // keys per tile
 constexpr int waves_per_simd(int RT, int D, bool FP8) {
   return RT == 1 && D * (FP8 ? 1 : 2) < 256 ? 2 : 1;
 }
+// Runs of one head at most: all its wavefronts on the chip, where there is but
+// one head (attn_layout).
+constexpr int kMaxRuns = kCus * 4 * 2;
+static_assert(waves_per_simd(1, 64, true) * kCus * 4 <= kMaxRuns, "the join's weights");
 
 struct AttnShape {
   int rows;        // G * Q
@@ -795,7 +796,6 @@ AttnLayout attn_layout(int64_t rows, int64_t Hkv, int64_t D, bool e4m3, bool pg)
   L.slot_rows = (int)(rows < L.RT * 16 ? rows : L.RT * 16);
   L.groups = kCus * 4 * waves_per_simd(L.RT, (int)D, e4m3) / L.NHV;
   if (L.groups < 1) L.groups = 1;
-  if (L.groups > kMaxRuns) L.groups = kMaxRuns;
   const size_t slots = (size_t)2 * L.groups * L.NHV;
   L.ml = 0;
   L.o = (slots * L.slot_rows * 2 * sizeof(float) + 255) & ~(size_t)255;
@@ -828,9 +828,8 @@ hipError_t launch_rt(const AttnArgs& a, AttnShape& sh, const AttnLayout& L, hipS
       return hipGetLastError();
     }
   }
-  const int64_t most = (keys + TK - 1) / TK * a.B;
-  sh.groups = (int)(most < a.B ? a.B : most < L.groups ? most : L.groups);
-  if (sh.groups > L.groups) sh.groups = L.groups;
+  const int64_t most = (keys + TK - 1) / TK * a.B;   // tiles
+  sh.groups = (int)(most < L.groups ? most : L.groups);
   const int64_t units = (int64_t)sh.groups * sh.NHV;
   hipLaunchKernelGGL((k_attn_runs<D, FP8, RT, PG>), dim3((uint32_t)((units + 3) / 4)), dim3(256),
                      0, stream, a, sh);

@@ -7,7 +7,7 @@
 // with x0, x1 at i and i + R/2 (half layout) or at 2i and 2i + 1
 // (interleaved); the rest of the head passes through. The product is formed
 // in 64 bits and reduced to a fraction of a turn there (at position 10^6 a
-// 32-bit product would be off by up to 0.06 rad), then sine and cosine are
+// 32-bit product would be off by up to 0.03 rad), then sine and cosine are
 // 32-bit.
 //
 // Bound: bytes for a prompt, latency for a token. A workgroup takes one token
