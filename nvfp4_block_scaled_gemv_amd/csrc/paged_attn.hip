@@ -28,7 +28,7 @@
 // the j-th equal part of them, whatever the lengths are. A sequence that lies
 // inside one run is finished there; others leave partial (m, sum, O) records,
 // at most two per wavefront, that k_attn_join adds in a fixed order. No
-// atomics. Where the table's rows are short (kWholeKeys), one workgroup of
+// atomics. Where the table's rows are short (whole_keys), one workgroup of
 // eight wavefronts takes a sequence and head whole and joins them in LDS.
 #include "elems.h"
 #include "internal.h"
@@ -38,14 +38,7 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kCus = 256;
-// The whole form: sequences of at most kWholeKeys keys, twice that where there
-// are kWholeMany workgroups or more. One sequence (32 / 8 heads of 128, bf16,
-// between two events): 12.4 us against 15.2 in two launches at 256 keys, 14.8
-// against 15.8 at 512, 18.8 against 16.1 at 1024; 64 of them at 1024: 56.7
-// against 55.6; 8 with 4 tokens each at 1024 (E4M3): 18.8 against 29.1.
-constexpr int kWholeWaves = 8;
-constexpr int kWholeKeys = 512;
-constexpr int kWholeMany = 64;
+constexpr int kWholeWaves = 8;   // wavefronts per workgroup of the whole form
 constexpr float kLog2e = 1.4426950408889634f;
 // The reference of the exponentials is moved only when a score passes it by
 // more than this (in powers of two): exp2 of at most 2^8 loses nothing in fp32
@@ -808,6 +801,32 @@ int capacity(const AttnArgs& a) {
   const int64_t cap = a.num_blocks ? a.max_blocks * a.page : 0;
   return (int)(cap < 0x7FFFFF00 ? cap : 0x7FFFFF00);
 }
+// The whole form takes tables of at most this many keys (a row's, or a
+// window's). It saves the join, but a wavefront reads 32 of every 256 keys one
+// after the other: about 4 us a turn in bf16 at heads of 128, half of it in E4M3
+// or at heads of 64. So few sequences take it for one such turn (2^16 bytes of a
+// head's keys); from 256 rows on, where the join's own work is more, for two;
+// where the workgroups fill the CUs, or half of them with 16 rows each, up to 1024
+// keys. More than 256 workgroups run in turns (their registers allow one per CU),
+// which only a long join pays for: with less than four rows each they take one
+// turn, and past 768 none. Whole against split in us, in graphs of 20
+// calls, 8 key-value heads of 128 if not said otherwise:
+//   1 token, G 4, bf16:   1 sequence 256 keys 7.1 / 9.5, 512 11.2 / 10.0;
+//                         8: 512 13.0 / 12.1, 1024 21.8 / 14.0; 16: 512 13.7 /
+//                         13.9, 1024 23.2 / 19.5; 32: 1024 27.2 / 30.1
+//   the same, E4M3:       1: 512 7.5 / 9.3, 1024 11.9 / 9.7; 8: 1024 13.1 / 14.3
+//   5 tokens, bf16:       1: 256 11.0 / 12.7, 512 15.7 / 13.4; 8: 512 17.5 / 21.2,
+//                         1024 25.8 / 23.0; 16: 1024 28.4 / 29.6
+//   pages of 20, 5 tokens: 1: 256 12.9 / 13.4, 512 22.3 / 14.2
+//   16 heads of 64, G 1:  1: 512 9.4 / 9.3; 8: 1024 15.9 / 13.9; 16: 17.6 / 19.8;
+//                         24: 512 18.2 / 17.2, 1024 31.1 / 25.3; 64: 128 16.4 / 15.3,
+//                         512 36.3 / 30.4
+int64_t whole_keys(const AttnArgs& a, const AttnShape& sh) {
+  const int64_t wgs = a.B * sh.NHV, one = (1 << 16) / (a.D * (a.cache_e4m3 ? 1 : 2));
+  if (wgs > kCus && sh.rows < 4) return wgs > 3 * kCus ? 0 : one;
+  if (wgs >= kCus || (wgs >= kCus / 2 && sh.rows >= 16)) return 1024;
+  return a.B * a.Q * a.Hq >= 256 && one < 1024 ? 2 * one : one;
+}
 // Keys that a sequence reads at most: by its table row, or by its window
 // (which starts at most a tile early).
 int64_t most_keys(const AttnArgs& a) {
@@ -822,7 +841,7 @@ hipError_t launch_rt(const AttnArgs& a, AttnShape& sh, const AttnLayout& L, hipS
   if (sh.cap == 0)
     return launch_fill_zero((float*)a.out, (size_t)(a.B * a.Q * a.Hq * D / 2), stream);
   if constexpr (D < 256) {   // heads of 256: their eight wavefronts' registers would spill
-    if (keys <= kWholeKeys * (a.B * sh.NHV >= kWholeMany ? 2 : 1)) {
+    if (keys <= whole_keys(a, sh)) {
       hipLaunchKernelGGL((k_attn_whole<D, FP8, RT, PG>), dim3((uint32_t)(a.B * sh.NHV)),
                          dim3(kWholeWaves * 64), 0, stream, a, sh);
       return hipGetLastError();
