@@ -496,7 +496,8 @@ typedef enum nvfp4_dtype {
  *   y[m, i]            = s[m, i] * rsqrt(mean_i s[m, i]^2 + eps) * weight[i]
  *
  * y comes from the fp32 s, not from its rounding, and is rounded once to bf16
- * (nvfp4_gemv's x). All sums are fp32, in an order that M and H fix.
+ * (nvfp4_gemv's x). All sums are fp32, in an order that the sizes and types of
+ * the call fix.
  *
  *   x             bf16 or fp32 (x_type NVFP4_BF16 / NVFP4_F32, a GEMV's y)
  *                 [M, H], 16-byte aligned;

@@ -223,11 +223,18 @@ hipError_t launch_v(const NormArgs& a, int W, hipStream_t stream) {
 template <typename TX, typename TR, int OUT>
 hipError_t launch_o(const NormArgs& a, hipStream_t stream) {
   // Groups of 8 per lane: one while the row fits 1024 threads that way, which
-  // is the shortest way through few rows (512 rows of 7168, NVFP4: 7.0 us, 9.8
-  // with four). From 1024 rows on fewer threads per row, so that more rows are
-  // in flight where one reduces: 8192 rows of 7168 fp32 to E4M3 71.4 -> 46.7 us,
-  // to bf16 64.0 -> 58.4; 16384 rows of 4096 to NVFP4 77.6 -> 65.6.
-  const int64_t vecs = a.H / 8, one = a.M >= 1024 ? 256 : 1024;
+  // is the shortest way through few rows. With many, fewer threads per row, so
+  // that more rows are in flight where one reduces and encodes. A residual's
+  // stores keep enough in flight without, so there only NVFP4 gains, later. Rows
+  // of 7168 with fewer threads against one group, us, other arrays each time:
+  //   fp32 to E4M3            1024 rows 11.0 / 12.2, 2048 17.0 / 21.1, 8192 54 / 69
+  //   bf16 to bf16            1024 7.4 / 8.2, 8192 44 / 53
+  //   bf16 + fp32 to E4M3     1024 21.5 / 20.9, 8192 120 / 117
+  //   bf16 to NVFP4           1024 13.1 / 12.6, 2048 19.9 / 21.3, 8192 56 / 76
+  //   fp32 + bf16 to NVFP4    1024 21.2 / 18.4, 2048 32.6 / 30.4, 4096 53.7 / 55.4
+  constexpr bool kRes = !__is_same(TR, None);
+  constexpr int64_t many = OUT == kOutNvfp4 ? (kRes ? 4096 : 2048) : kRes ? INT64_MAX : 1024;
+  const int64_t vecs = a.H / 8, one = a.M >= many ? 256 : 1024;
   const int VPT = vecs <= one ? 1 : vecs <= 2 * one ? 2 : 4;
   const int W = (int)((vecs + 64 * VPT - 1) / (64 * VPT));
   return VPT == 1   ? launch_v<TX, TR, OUT, 1>(a, W, stream)
