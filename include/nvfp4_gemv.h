@@ -62,6 +62,9 @@
 extern "C" {
 #endif
 
+/* The operators of a decode step (from nvfp4_add_rmsnorm on) joined version 9
+   without changing what it had: a program that may meet a library without them
+   looks one of their symbols up. */
 #define NVFP4_ABI_VERSION 9
 
 /* Largest number of activation rows (tokens) one dense GEMV call takes (the

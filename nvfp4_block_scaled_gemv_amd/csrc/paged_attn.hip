@@ -771,9 +771,13 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnS
 }
 
 // Row tiles of 16 in one pass; a head with more rows is read again for the
-// others. Heads of 256 take two only where pages hold whole runs of 16 keys
-// (pg): 8 sequences of 20000 keys, 32 rows, 220 -> 170 us; without, one offset
-// per lane and key spills registers (40 rows, pages of 20: 108 -> 163 us).
+// others. One against two, 8 sequences, bf16: 20000 keys, 8 heads of 128 with 20
+// rows 210 / 114 us, 8192 keys with 64 rows 186 / 103, with 256 rows 557 / 336 (the
+// row tiles of a head are neighbouring wavefronts, but their loads carry the
+// streaming hint all the same). Heads of 256 take two where pages hold whole
+// runs of 16 keys (pg): 20000 keys, 8 heads with 20 rows 387 / 241, 2 heads with 32
+// rows 112 / 102, though the bf16 form spills 45 VGPRs. Without, one offset per
+// lane and key spills more than it saves (40 rows, pages of 20: 108 / 163 us).
 int row_tiles(int64_t rows, int64_t D, bool pg) { return rows <= 16 || (D == 256 && !pg) ? 1 : 2; }
 
 // The most runs per head (all heads' together fill the SIMDs), and where their
@@ -840,7 +844,10 @@ hipError_t launch_rt(const AttnArgs& a, AttnShape& sh, const AttnLayout& L, hipS
   // no page at all: every sequence is empty
   if (sh.cap == 0)
     return launch_fill_zero((float*)a.out, (size_t)(a.B * a.Q * a.Hq * D / 2), stream);
-  if constexpr (D < 256) {   // heads of 256: their eight wavefronts' registers would spill
+  // Heads of 256 have no whole form: eight wavefronts leave 256 registers each,
+  // which two row tiles of 128 fill already (6 to 55 VGPRs spill in three of the
+  // four; their times are in whole_keys).
+  if constexpr (D < 256) {
     if (keys <= whole_keys(a, sh)) {
       hipLaunchKernelGGL((k_attn_whole<D, FP8, RT, PG>), dim3((uint32_t)(a.B * sh.NHV)),
                          dim3(kWholeWaves * 64), 0, stream, a, sh);
