@@ -31,6 +31,7 @@
 // atomics. Where the table's rows are short (whole_keys), one workgroup of
 // eight wavefronts takes a sequence and head whole and joins them in LDS.
 #include "elems.h"
+#include "attn_span.h"
 #include "internal.h"
 
 namespace nvfp4 {
@@ -46,7 +47,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;
 // s_waitcnt vmcnt(0), no other counter.
 constexpr int kVmcnt0 = 0x0F70;
-constexpr int TK = 32;   // keys per tile
 // Wavefronts per SIMD of the split form. Few long streams read memory best:
 // heads of 256 bytes and more keep 16 KB and more in flight per wavefront with
 // one; smaller heads need two.
@@ -72,17 +72,8 @@ struct AttnShape {
 
 typedef const __attribute__((address_space(4))) int32_t* const_i32;
 
-// The tiles of one sequence: keys base .. len - 1.
-struct Span {
-  int len, base, n;   // n >= 1: an empty sequence has one tile, of which nobody sees a key
-};
 __device__ __forceinline__ Span span_of(const AttnArgs& a, const AttnShape& sh, int len) {
-  Span s;
-  s.len = len < 0 ? 0 : len > sh.cap ? sh.cap : len;
-  const int64_t lo = a.window ? (int64_t)s.len - a.Q - a.window + 1 : 0;
-  s.base = lo <= 0 ? 0 : (int)lo & ~(TK - 1);
-  s.n = s.len > s.base ? (s.len - s.base + TK - 1) / TK : 1;
-  return s;
+  return nvfp4::span_of(len, sh.cap, a.Q, a.window);
 }
 
 // Inclusive sums over the 64 lanes, by DPP: within rows of 16, then from each
@@ -315,22 +306,20 @@ struct AttnWave {
   // last sequence: any tile, it is not computed).
   __device__ __forceinline__ Cursor after(const Cursor& c, int step) {
     if (c.left <= step && c.b + 1 < (int)a.B) return first_of(c.b + 1, len_after, 0);
-    return Cursor{c.b, c.len, c.key + step * TK, c.left - step};
+    return Cursor{c.b, c.len, tile_after(c.key, step), c.left - step};
   }
 
-  __device__ __forceinline__ int page_of(int key, int& in) const {
-    const int pi = sh.page_shift >= 0 ? key >> sh.page_shift : key / (int)a.page;
-    in = key - pi * (int)a.page;
-    return pi < (int)a.max_blocks ? pi : (int)a.max_blocks - 1;
+  __device__ __forceinline__ int page_of(int key, int ahead, int& in) const {
+    return nvfp4::page_of(key, ahead, (int)a.page, sh.page_shift, (int)a.max_blocks, in);
   }
   // Only for tiles that hold a key: an empty sequence's table has no row.
   __device__ __forceinline__ void fetch(const Cursor& c) {
     if constexpr (PG) {
       const const_i32 table = (const_i32)(uintptr_t)(a.table + (int64_t)c.b * a.max_blocks);
 #pragma unroll
-      for (int u = 0; u < NU; ++u) ids[u] = table[page_of(c.key + 16 * u, in_page[u])];
+      for (int u = 0; u < NU; ++u) ids[u] = table[page_of(c.key, 16 * u, in_page[u])];
     } else {
-      const int pi = page_of(c.key + (lane & (TK - 1)), in_page[0]);
+      const int pi = page_of(c.key, lane & (TK - 1), in_page[0]);
       ids[0] = a.table[(int64_t)c.b * a.max_blocks + pi];
     }
   }
@@ -803,7 +792,7 @@ AttnLayout attn_layout(int64_t rows, int64_t Hkv, int64_t D, bool e4m3, bool pg)
 // Keys that a row of the table can name (none where there is no page).
 int capacity(const AttnArgs& a) {
   const int64_t cap = a.num_blocks ? a.max_blocks * a.page : 0;
-  return (int)(cap < 0x7FFFFF00 ? cap : 0x7FFFFF00);
+  return (int)(cap < 0x7FFFFFFF ? cap : 0x7FFFFFFF);
 }
 // The whole form takes tables of at most this many keys (a row's, or a
 // window's). It saves the join, but a wavefront reads 32 of every 256 keys one
@@ -845,7 +834,7 @@ hipError_t launch_rt(const AttnArgs& a, AttnShape& sh, const AttnLayout& L, hipS
   if (sh.cap == 0)
     return launch_fill_zero((float*)a.out, (size_t)(a.B * a.Q * a.Hq * D / 2), stream);
   // Heads of 256 have no whole form: eight wavefronts leave 256 registers each,
-  // which two row tiles of 128 fill already (6 to 55 VGPRs spill in three of the
+  // which two row tiles of 128 fill already (4 to 53 VGPRs spill in three of the
   // four; their times are in whole_keys).
   if constexpr (D < 256) {
     if (keys <= whole_keys(a, sh)) {
