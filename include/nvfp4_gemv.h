@@ -510,7 +510,8 @@ typedef enum nvfp4_dtype {
  *                 (in place), must not overlap it otherwise;
  *   weight        bf16[H], 16-byte aligned;  eps  finite, >= 0;
  *   M             0 <= M <= NVFP4_MAX_ROWS;
- *   H             0 <= H <= NVFP4_NORM_MAX_H, H % 8 == 0;
+ *   H             0 <= H <= NVFP4_NORM_MAX_H, H % 8 == 0; nothing is written
+ *                 where M or H is 0;
  *   y             bf16[M, H] out, 16-byte aligned.
  * Errors: NULL, SHAPE (a type that is not allowed and eps included), ALIGN,
  * UNSUPPORTED, ALIAS, HIP.

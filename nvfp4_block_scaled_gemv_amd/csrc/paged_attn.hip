@@ -402,7 +402,8 @@ struct AttnWave {
   // outputs over 1277 keys 20 rounded the other way, 2 with three. The third
   // takes a half more of these products: 5 tokens on 32773 keys 27.8 -> 28.3 us,
   // 700 keys 6.2 -> 6.3, a short batch with two row tiles 16.3 -> 17.3.
-  __device__ __forceinline__ void softmax(const f32x4_t (&S)[RT][NU], u32x4_t (&pf)[kParts][RT][NP]) {
+  __device__ __forceinline__ void softmax(const f32x4_t (&S)[RT][NU],
+                                          u32x4_t (&pf)[kParts][RT][NP]) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       float mx = -INFINITY;

@@ -14,10 +14,10 @@
 // give one number each. Two launches: k_verify_sums, a workgroup per 1024
 // values of the row, finds the row (every workgroup for itself: a gather of Q
 // numbers) and sums its piece; k_verify_draw, a workgroup per sequence, finds
-// the piece that holds the border, then the token in it. A second launch costs
-// less than a workgroup that waits for the others' sums. Measured: one sequence
-// of 4 drafts, 151936 entries: 3.5 + 3.6 us, each the latency of two dependent
-// loads; 16 of them with draft probabilities, 19.4 MB: 6.4 + 4.3 us.
+// the piece that holds the border, then the token in it (the workspace may hold
+// anything, so the sums' workgroups cannot count their arrivals in it). Measured:
+// one sequence of 4 drafts, 151936 entries: 3.6 + 3.6 us, each the latency of two
+// dependent loads; 16 of them with draft probabilities, 19.4 MB: 7.6 + 5.1 us.
 #include "elems.h"
 #include "internal.h"
 
