@@ -801,10 +801,10 @@ int capacity(const AttnArgs& a) {
 // or at heads of 64. So few sequences take it for one such turn (2^16 bytes of a
 // head's keys); from 256 rows on, where the join's own work is more, for two;
 // where the workgroups fill the CUs, or half of them with 16 rows each, up to 1024
-// keys. More than 256 workgroups run in turns (their registers allow one per CU),
-// which only a long join pays for: with less than four rows each they take one
-// turn, and past 768 none. Whole against split in us, in graphs of 20
-// calls, 8 key-value heads of 128 if not said otherwise:
+// keys. More than 256 workgroups run one after the other (their registers allow
+// one per CU, or two), which only a long join pays for: with less than four rows
+// each they take tables of one turn, and past 768 none. Whole against split in
+// us, in graphs of 20 calls, 8 key-value heads of 128 if not said otherwise:
 //   1 token, G 4, bf16:   1 sequence 256 keys 7.1 / 9.5, 512 11.2 / 10.0;
 //                         8: 512 13.0 / 12.1, 1024 21.8 / 14.0; 16: 512 13.7 /
 //                         13.9, 1024 23.2 / 19.5; 32: 1024 27.2 / 30.1
