@@ -5,8 +5,9 @@
  * expert-slot variant for M <= 8 (gather top-k experts by id, SwiGLU,
  * combine by gate weight), and the parts of a decode step that stand between
  * these products: RMS norm with the residual, rotary positions with the
- * append to a paged key-value cache, attention over that cache, and the
- * verification of drafted tokens.
+ * append to a paged key-value cache (bf16, E4M3 or NVFP4), attention over that
+ * cache, low-rank adapters beside the products, and the verification of drafted
+ * tokens.
  *
  * The operations are the ones the GLM-5.3-Flash-NVFP4 blueprint pages
  * describe for their decode step:
@@ -63,8 +64,9 @@ extern "C" {
 #endif
 
 /* The operators of a decode step (from nvfp4_add_rmsnorm on) joined version 9
-   without changing what it had: a program that may meet a library without them
-   looks one of their symbols up. */
+   without changing what it had, and after them the NVFP4 cache, the scored
+   attention and the adapters (nvfp4_lora_segments): a program that may meet a
+   library without them looks one of their symbols up. */
 #define NVFP4_ABI_VERSION 9
 
 /* Largest number of activation rows (tokens) one dense GEMV call takes (the
@@ -625,6 +627,56 @@ nvfp4_status nvfp4_rope_append(const void* q, int64_t q_stride, const void* k, i
                                int64_t R, int interleaved, float rope_scale, uint16_t* q_out,
                                const nvfp4_kv_cache* cache, hipStream_t stream);
 
+/*
+ * nvfp4_kv_cache4 -- a paged key-value cache in NVFP4: as nvfp4_kv_cache, an
+ * element being e2m1(code) * e4m3(scale) * g with a code of 4 bits, a scale for
+ * each 16 consecutive elements of a head and one g for all keys (values).
+ *
+ *   k, v              codes: element d of (block, token, head) is in byte block *
+ *                     stride_block + token * stride_token + head * stride_head +
+ *                     d / 2, in bits 3..0 for even d, 7..4 for odd d. 16-byte
+ *                     aligned, strides (bytes) >= D / 2 and multiples of 16,
+ *                     stride_token < 2^26;
+ *   k_scales, v_scales  E4M3 bytes, that of elements 16 b .. 16 b + 15 at block *
+ *                     scale_stride_block + .. + b. 4-byte aligned, strides
+ *                     (bytes) >= D / 16 and multiples of 4, scale_stride_token <
+ *                     2^26. No two elements or scales may share an address (not
+ *                     checked);
+ *   k_gscale, v_gscale  device float[1], > 0 and finite (not checked);
+ *   D                 a multiple of 64; page, num_blocks as in nvfp4_kv_cache.
+ * The structure is read on the host during the call.
+ */
+typedef struct nvfp4_kv_cache4 {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  const float* k_gscale;
+  const float* v_gscale;
+  int64_t num_blocks, page, n_kv_heads, D;
+  int64_t stride_block, stride_token, stride_head;
+  int64_t scale_stride_block, scale_stride_token, scale_stride_head;
+} nvfp4_kv_cache4;
+
+/*
+ * nvfp4_rope_append_nvfp4 -- nvfp4_rope_append to an NVFP4 cache. The blocks of
+ * 16 elements are quantised from the fp32 results of the rotation (v: from v)
+ * as nvfp4_quantize_act does with the static scale *k_gscale (*v_gscale): scale
+ * = E4M3(amax / (6 g)), code = E2M1(x / (scale g)), both to nearest even and
+ * saturating (an infinite element gives a scale of 448). A block that holds a
+ * NaN gets the scale NaN (0x7F) and codes 0.
+ *
+ *   cache   not NULL; D a multiple of 64.
+ * Everything else as nvfp4_rope_append.
+ */
+nvfp4_status nvfp4_rope_append_nvfp4(const void* q, int64_t q_stride, const void* k,
+                                     int64_t k_stride, const void* v, int64_t v_stride,
+                                     int x_type, const int64_t* positions, const int64_t* slots,
+                                     const float* inv_freq, int64_t T, int64_t Hq, int64_t D,
+                                     int64_t R, int interleaved, float rope_scale,
+                                     uint16_t* q_out, const nvfp4_kv_cache4* cache,
+                                     hipStream_t stream);
+
 /* Largest number of sequences, and of new tokens per sequence, of one
    nvfp4_paged_attention call. */
 #define NVFP4_ATTN_MAX_B 4096
@@ -633,8 +685,9 @@ nvfp4_status nvfp4_rope_append(const void* q, int64_t q_stride, const void* k, i
 /*
  * nvfp4_paged_attention_workspace_bytes -- device workspace that
  * nvfp4_paged_attention needs: the partial sums of the workgroups that share a
- * sequence and head. It does not grow with the lengths. 0 for sizes that the
- * call refuses.
+ * sequence and head. It does not grow with the lengths, and holds for
+ * nvfp4_paged_attention_scored and nvfp4_paged_attention_nvfp4 too. 0 for sizes
+ * that the call refuses.
  */
 size_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv,
                                              int64_t D);
@@ -681,6 +734,111 @@ nvfp4_status nvfp4_paged_attention(const uint16_t* q, const nvfp4_kv_cache* cach
                                    int64_t B, int64_t Q, int64_t Hq, int64_t max_blocks,
                                    float scale, int64_t window, uint16_t* out, void* workspace,
                                    size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * nvfp4_attn_scores -- what a call does to the scores z = scale * q . K before
+ * the softmax: first the cap, then the bias by distance (token at p, key at j):
+ *
+ *   z = softcap * tanh(z / softcap)     (softcap > 0)
+ *   z = z + slopes[head] * (j - p)      (slopes != NULL)
+ *
+ *   softcap  0 (none) or 1e-6 .. 1e30; tanh is within 2^-22 of its value;
+ *   slopes   device float[Hq], finite (not checked), or NULL. Positive slopes
+ *            weigh far keys less.
+ * The structure is read on the host during the call.
+ */
+typedef struct nvfp4_attn_scores {
+  float softcap;
+  const float* slopes;
+} nvfp4_attn_scores;
+
+/*
+ * nvfp4_paged_attention_scored -- nvfp4_paged_attention with scores that are
+ * capped, or get a bias by distance, or both. scores: NULL for neither.
+ * Everything else as nvfp4_paged_attention.
+ */
+nvfp4_status nvfp4_paged_attention_scored(const uint16_t* q, const nvfp4_kv_cache* cache,
+                                          const int32_t* block_table, const int32_t* seq_lens,
+                                          int64_t B, int64_t Q, int64_t Hq, int64_t max_blocks,
+                                          float scale, int64_t window,
+                                          const nvfp4_attn_scores* scores, uint16_t* out,
+                                          void* workspace, size_t workspace_bytes,
+                                          hipStream_t stream);
+
+/*
+ * nvfp4_paged_attention_nvfp4 -- nvfp4_paged_attention (scored, where scores is
+ * not NULL) over an NVFP4 cache, D 64, 128 or 256.
+ *
+ * A code times its block's scale is exact in fp16, which the products take. A
+ * row of q enters them times a power of two that takes its largest element to
+ * 2^14 or more: elements down to 2^-31 of that one whole, others to within 2^-39
+ * of it. Probabilities enter the product with V as the sum of two fp16: within
+ * 2^-24 of each, or 2^-36 of the row's largest. Scores, maxima, sums and
+ * probabilities are fp32. A NaN scale byte stands for 16 NaN elements.
+ * Everything else as nvfp4_paged_attention.
+ */
+nvfp4_status nvfp4_paged_attention_nvfp4(const uint16_t* q, const nvfp4_kv_cache4* cache,
+                                         const int32_t* block_table, const int32_t* seq_lens,
+                                         int64_t B, int64_t Q, int64_t Hq, int64_t max_blocks,
+                                         float scale, int64_t window,
+                                         const nvfp4_attn_scores* scores, uint16_t* out,
+                                         void* workspace, size_t workspace_bytes,
+                                         hipStream_t stream);
+
+/* Largest rank, and number of adapters, of one nvfp4_lora_segments call. */
+#define NVFP4_LORA_MAX_RANK 256
+#define NVFP4_LORA_MAX_ADAPTERS (1 << 20)
+
+/* One projection's adapters in nvfp4_lora_segments. */
+typedef struct nvfp4_lora_segment {
+  const uint16_t* a;   /* bf16[n_adapters, rank, K], 16-byte aligned */
+  const uint16_t* b;   /* bf16[n_adapters, N, rank], 16-byte aligned */
+  const float* base;   /* [M, N]: what the projection gave; may be y itself;
+                          NULL: zeros */
+  float* y;            /* [M, N] out */
+  int64_t N;           /* >= 0; a segment with N == 0 is skipped */
+} nvfp4_lora_segment;
+
+/*
+ * nvfp4_lora_workspace_bytes -- device workspace of nvfp4_lora_segments: sums
+ * of A x over pieces of K. 0 for sizes that the call refuses.
+ */
+size_t nvfp4_lora_workspace_bytes(int64_t M, int64_t K, int64_t rank, int64_t n_segments);
+
+/*
+ * nvfp4_lora_segments -- low-rank adapters of many requests at once beside
+ * projections that share x (nvfp4_gemv, nvfp4_gemv_segments). For every segment
+ * s and row m, with e = ids[m]:
+ *
+ *   y_s[m, :] = base_s[m, :] + alpha[e] * B_s[e] (A_s[e] x[m])
+ *
+ * and y_s[m] = base_s[m] where e is outside [0, n_adapters) (a request without
+ * an adapter: -1). A x is summed in fp32 and enters the product with B whole
+ * (as the sum of three bf16: an infinite one gives NaN). Rows that share an
+ * adapter need not be neighbours; up to 16 of them read it once.
+ *
+ *   segs        host array, read during the call; device pointers inside;
+ *   n_segments  0 .. NVFP4_MAX_SEGMENTS; their N together at most NVFP4_MAX_N;
+ *   n_adapters  0 .. NVFP4_LORA_MAX_ADAPTERS;
+ *   rank        a multiple of 8, 8 .. NVFP4_LORA_MAX_RANK;
+ *   ids         int32[M];
+ *   ranks       int32[n_adapters], or NULL: how many of an adapter's ranks are
+ *               its own (taken into 0 .. rank); A's rows and B's columns past
+ *               them may hold anything;
+ *   alpha       float[n_adapters] or NULL: 1 for all;
+ *   x           bf16[M, K], 16-byte aligned;
+ *   M, K        as for nvfp4_gemv (M <= NVFP4_MAX_M, K % 32 == 0);
+ *   workspace   at least nvfp4_lora_workspace_bytes(M, K, rank, n_segments)
+ *               bytes, 256-byte aligned; overwritten, its content does not
+ *               matter; must not be shared by calls that may run concurrently.
+ * base may be its own segment's y; no output may overlap anything else. Two
+ * launches. Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, WORKSPACE, ALIAS, HIP.
+ */
+nvfp4_status nvfp4_lora_segments(const nvfp4_lora_segment* segs, int64_t n_segments,
+                                 int64_t n_adapters, int64_t rank, const int32_t* ids,
+                                 const int32_t* ranks, const float* alpha, const uint16_t* x,
+                                 int64_t M, int64_t K, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
 
 /* Largest number of drafts per sequence, of sequences and of vocabulary
    entries of one nvfp4_verify_draft call. */

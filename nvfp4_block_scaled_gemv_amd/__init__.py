@@ -22,9 +22,14 @@ Functions (same names as the C entry points, without the prefix):
   add_rmsnorm_e4m3(x, weight, eps[, residual, group]) -> y8, scales, residual_out
   add_rmsnorm_nvfp4(x, weight, eps, gscale[, residual]) -> codes, scales, residual_out
   rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, ...) -> q_out (bf16)
+  rope_append_nvfp4(q, k, v, positions, slots, inv_freq, k_cache, v_cache, ...) -> q_out (bf16)
   paged_attention(q, k_cache, v_cache, block_table, seq_lens, ...) -> out (bf16)
+  paged_attention_scored(q, k_cache, v_cache, block_table, seq_lens, softcap, slopes, ...) -> out
+  paged_attention_nvfp4(q, k_cache, v_cache, block_table, seq_lens, ...) -> out (bf16)
+  lora_segments([(a, b), ...], x, ids[, bases, alpha, ranks]) -> [y_s] (fp32 [M, N_s])
   verify_draft(target_p, draft_p, draft, u_accept, u_sample, ...) -> tokens, n_accepted
-  paged_attention_workspace_bytes(B, Q, Hq, Hkv, D), verify_draft_workspace_bytes(B, V)
+  paged_attention_workspace_bytes(B, Q, Hq, Hkv, D), verify_draft_workspace_bytes(B, V),
+  lora_workspace_bytes(M, K, rank, n_segments)
   stream_read(buf, sink)                 (measurement aid: one pure read of buf)
 The ``*_into`` variants write into caller-provided outputs.
 """
@@ -61,6 +66,9 @@ ATTN_MAX_Q = 64
 VERIFY_MAX_Q = 63
 VERIFY_MAX_B = 4096
 VERIFY_MAX_V = 1 << 24
+# NVFP4_LORA_MAX_RANK, NVFP4_LORA_MAX_ADAPTERS.
+LORA_MAX_RANK = 256
+LORA_MAX_ADAPTERS = 1 << 20
 # NVFP4_NOALLOC_SCRATCH_BYTES: the device array of nvfp4_moe_gemv_noalloc.
 NOALLOC_SCRATCH_BYTES = 4 << 20
 
@@ -99,6 +107,28 @@ class KvCache(ctypes.Structure):
                 ("page", ctypes.c_int64), ("n_kv_heads", ctypes.c_int64), ("D", ctypes.c_int64),
                 ("stride_block", ctypes.c_int64), ("stride_token", ctypes.c_int64),
                 ("stride_head", ctypes.c_int64), ("type", ctypes.c_int)]
+
+
+class KvCache4(ctypes.Structure):
+    """nvfp4_kv_cache4: a paged key-value cache in NVFP4."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("k_gscale", ctypes.c_void_p),
+                ("v_gscale", ctypes.c_void_p), ("num_blocks", ctypes.c_int64),
+                ("page", ctypes.c_int64), ("n_kv_heads", ctypes.c_int64), ("D", ctypes.c_int64),
+                ("stride_block", ctypes.c_int64), ("stride_token", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64), ("scale_stride_block", ctypes.c_int64),
+                ("scale_stride_token", ctypes.c_int64), ("scale_stride_head", ctypes.c_int64)]
+
+
+class AttnScores(ctypes.Structure):
+    """nvfp4_attn_scores: the cap and the bias of attention's scores."""
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p)]
+
+
+class LoraSegment(ctypes.Structure):
+    """nvfp4_lora_segment: one projection's adapters."""
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("base", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("N", ctypes.c_int64)]
 
 
 # nvfp4_dtype
@@ -175,6 +205,21 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_paged_attention.argtypes = [_VP, ctypes.POINTER(KvCache), _VP, _VP, _I64, _I64,
                                             _I64, _I64, ctypes.c_float, _I64, _VP, _VP,
                                             ctypes.c_size_t, _VP]
+        L.nvfp4_rope_append_nvfp4.restype = ctypes.c_int
+        L.nvfp4_rope_append_nvfp4.argtypes = ([_VP, _I64] * 3 + [ctypes.c_int] + [_VP] * 3 +
+                                              [_I64] * 4 + [ctypes.c_int, ctypes.c_float, _VP,
+                                                            ctypes.POINTER(KvCache4), _VP])
+        for name, cache in (("scored", KvCache), ("nvfp4", KvCache4)):
+            f = getattr(L, "nvfp4_paged_attention_" + name)
+            f.restype = ctypes.c_int
+            f.argtypes = [_VP, ctypes.POINTER(cache), _VP, _VP, _I64, _I64, _I64, _I64,
+                          ctypes.c_float, _I64, ctypes.POINTER(AttnScores), _VP, _VP,
+                          ctypes.c_size_t, _VP]
+        L.nvfp4_lora_workspace_bytes.restype = ctypes.c_size_t
+        L.nvfp4_lora_workspace_bytes.argtypes = [_I64] * 4
+        L.nvfp4_lora_segments.restype = ctypes.c_int
+        L.nvfp4_lora_segments.argtypes = [ctypes.POINTER(LoraSegment), _I64, _I64, _I64, _VP, _VP,
+                                          _VP, _VP, _I64, _I64, _VP, ctypes.c_size_t, _VP]
         L.nvfp4_verify_draft_workspace_bytes.restype = ctypes.c_size_t
         L.nvfp4_verify_draft_workspace_bytes.argtypes = [_I64, _I64]
         L.nvfp4_verify_draft.restype = ctypes.c_int
@@ -782,13 +827,22 @@ def rope_append_into(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cach
     inv_freq fp32 [R / 2] turns the first R elements of each head. q and q_out
     may be None (only append); k, v, slots and the caches may be (only
     rotate)."""
+    c = None if k_cache is None or v_cache is None else \
+        (lambda: _kv_cache(k_cache, v_cache, k_scale, v_scale))
+    _rope_append("nvfp4_rope_append", q, k, v, positions, slots, inv_freq, q_out, c,
+                 (k_cache, v_cache, k_scale, v_scale), interleaved, rope_scale)
+
+
+def _rope_append(fn, q, k, v, positions, slots, inv_freq, q_out, make_cache, parts, interleaved,
+                 rope_scale) -> None:
+    """The call of either append; make_cache gives the cache's descriptor (None:
+    there is no cache), parts are its tensors."""
     x = k if q is None else q
     if x is None:
         raise ValueError("neither q nor k is given")
-    if (k is None) != (v is None) or (k is not None and (k_cache is None or v_cache is None)):
+    if (k is None) != (v is None) or (k is not None and make_cache is None):
         raise ValueError("k, v and the caches go together")
-    _same_device(x.get_device(), q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache,
-                 k_scale, v_scale)
+    _same_device(x.get_device(), q, k, v, positions, slots, inv_freq, q_out, *parts)
     xt = _ACT_TYPES.get(x.dtype)
     if xt is None:
         raise TypeError(f"q, k and v must be bf16 or fp32, got {x.dtype}")
@@ -811,7 +865,7 @@ def rope_append_into(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cach
         if T == 1:   # one token's stride says nothing
             qs = Hq * D
     if k is not None:
-        c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+        c = make_cache()
         Hkv, st, sv = c.n_kv_heads, k.stride(), v.stride()
         if k.dtype is not x.dtype or v.dtype is not x.dtype or k.shape != (T, Hkv, D) \
                 or v.shape != k.shape or c.D != D:
@@ -826,7 +880,7 @@ def rope_append_into(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cach
         if T == 1:
             ks = vs = Hkv * D
         cache = ctypes.byref(c)
-    _check("nvfp4_rope_append", lib().nvfp4_rope_append(
+    _check(fn, getattr(lib(), fn)(
         qp, qs or 0, kp, ks or 0, vp, vs or 0, xt, positions.data_ptr(), sp,
         inv_freq.data_ptr(), T, Hq, D, 2 * inv_freq.shape[0], 1 if interleaved else 0,
         rope_scale, op, cache, _stream(x)))
@@ -838,6 +892,56 @@ def rope_append(q, k, v, positions, slots, inv_freq, k_cache, v_cache, k_scale=N
     q_out = None if q is None else torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     rope_append_into(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache, k_scale,
                      v_scale, interleaved, rope_scale)
+    return q_out
+
+
+def _kv_cache4(k_cache, v_cache) -> KvCache4:
+    """The descriptor of an NVFP4 cache: two triples (codes u8 [blocks, page,
+    heads, D / 2], scales u8 [blocks, page, heads, D / 16], gscale fp32 [1]), any
+    strides with contiguous bytes, the same for both."""
+    (kc, ks, kg), (vc, vs, vg) = k_cache, v_cache
+    if kc.dtype is not torch.uint8 or vc.dtype is not torch.uint8 \
+            or ks.dtype is not torch.uint8 or vs.dtype is not torch.uint8 \
+            or kg.dtype is not torch.float32 or vg.dtype is not torch.float32 \
+            or kg.numel() != 1 or vg.numel() != 1:
+        raise TypeError("codes and scales must be uint8, gscale fp32 [1]")
+    if kc.dim() != 4 or vc.shape != kc.shape or vs.shape != ks.shape \
+            or ks.shape != (*kc.shape[:3], kc.shape[3] // 8) or kc.shape[3] % 32:
+        raise ValueError("codes must be [blocks, page, heads, D / 2], D a multiple of 64, and "
+                         "scales [blocks, page, heads, D / 16]")
+    for a, b in ((kc, vc), (ks, vs)):
+        st, sv = a.stride(), b.stride()
+        # the stride of a dimension of one says nothing
+        if st[3] != 1 or sv[3] != 1 or \
+                (sv != st and any(n > 1 and x != y for n, x, y in zip(a.shape, st, sv))):
+            raise ValueError("codes (scales) of k and v must have the same strides, the last one 1")
+    nb, page, heads, half = kc.shape
+    st, ss = kc.stride(), ks.stride()
+
+    def strides(s, n):   # (of a dimension of one: any that is allowed)
+        any_ = (n + 15) // 16 * 16
+        return (s[0] if nb > 1 else any_, s[1] if page > 1 else any_, s[2] if heads > 1 else any_)
+    return KvCache4(kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), kg.data_ptr(),
+                    vg.data_ptr(), nb, page, heads, 2 * half, *strides(st, half),
+                    *strides(ss, half // 8))
+
+
+def rope_append_nvfp4_into(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache,
+                           interleaved: bool = False, rope_scale: float = 1.0) -> None:
+    """rope_append_into with an NVFP4 cache: k_cache and v_cache are triples
+    (codes u8 [blocks, page, Hkv, D / 2], scales u8 [blocks, page, Hkv, D / 16],
+    gscale fp32 [1])."""
+    _rope_append("nvfp4_rope_append_nvfp4", q, k, v, positions, slots, inv_freq, q_out,
+                 lambda: _kv_cache4(k_cache, v_cache), (*k_cache, *v_cache), interleaved,
+                 rope_scale)
+
+
+def rope_append_nvfp4(q, k, v, positions, slots, inv_freq, k_cache, v_cache,
+                      interleaved: bool = False, rope_scale: float = 1.0):
+    """q_out (bf16 [T, Hq, D]; None without q)."""
+    q_out = None if q is None else torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    rope_append_nvfp4_into(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache,
+                           interleaved, rope_scale)
     return q_out
 
 
@@ -854,37 +958,161 @@ def paged_attention_into(q, k_cache, v_cache, block_table, seq_lens, out, worksp
     block_table int32 [B, max_blocks]; seq_lens int32 [B], the new tokens
     included; scale defaults to D ** -0.5; window > 0: each token sees the
     last `window` keys up to itself."""
-    _same_device(q.get_device(), k_cache, v_cache, block_table, seq_lens, out, workspace, k_scale,
-                 v_scale)
+    _paged_attention("nvfp4_paged_attention", q, lambda: _kv_cache(k_cache, v_cache, k_scale, v_scale),
+                     (k_cache, v_cache, k_scale, v_scale), block_table, seq_lens, out, workspace,
+                     scale, window)
+
+
+def _paged_attention(fn, q, make_cache, parts, block_table, seq_lens, out, workspace, scale,
+                     window, *scores) -> None:
+    """The call of any attention; make_cache gives the cache's descriptor, parts
+    are its tensors (and the slopes)."""
+    _same_device(q.get_device(), block_table, seq_lens, out, workspace, *parts)
     if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 \
             or block_table.dtype is not torch.int32 or seq_lens.dtype is not torch.int32:
         raise TypeError("q and out must be bf16, block_table and seq_lens int32")
     _contiguous(q, out, block_table, seq_lens, workspace)
-    c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    c = make_cache()
     T, Hq, D = q.shape
     B, width = block_table.shape
     if seq_lens.shape != (B,) or out.shape != q.shape or D != c.D or (T % B if B else T):
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, out {tuple(out.shape)}, "
                          f"block_table {tuple(block_table.shape)}, seq_lens "
                          f"{tuple(seq_lens.shape)}, D {c.D}")
-    _check("nvfp4_paged_attention", lib().nvfp4_paged_attention(
+    _check(fn, getattr(lib(), fn)(
         q.data_ptr(), ctypes.byref(c), block_table.data_ptr(), seq_lens.data_ptr(), B,
-        T // B if B else 0, Hq, width, D ** -0.5 if scale is None else scale, window,
+        T // B if B else 0, Hq, width, D ** -0.5 if scale is None else scale, window, *scores,
         out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(q)))
 
 
 def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale: float | None = None,
                     window: int = 0, k_scale=None, v_scale=None,
                     workspace: torch.Tensor | None = None) -> torch.Tensor:
-    T, Hq, D = q.shape
-    B = block_table.shape[0]
-    if workspace is None:
-        n = paged_attention_workspace_bytes(B, T // B if B else 0, Hq, k_cache.shape[2], D)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
-    out = torch.empty_like(q)
+    workspace, out = _attn_outputs(q, block_table, k_cache.shape[2], workspace)
     paged_attention_into(q, k_cache, v_cache, block_table, seq_lens, out, workspace, scale,
                          window, k_scale, v_scale)
     return out
+
+
+def _attn_outputs(q, block_table, Hkv, workspace):
+    """The workspace of an attention call (a new one where None is given) and its
+    output."""
+    T, Hq, D = q.shape
+    B = block_table.shape[0]
+    if workspace is None:
+        n = paged_attention_workspace_bytes(B, T // B if B else 0, Hq, Hkv, D)
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=q.device)
+    return workspace, torch.empty_like(q)
+
+
+def _scores(softcap, slopes, Hq):
+    """nvfp4_attn_scores (None: neither cap nor bias)."""
+    if slopes is not None:
+        if slopes.dtype is not torch.float32 or slopes.shape != (Hq,) \
+                or not slopes.is_contiguous():
+            raise ValueError(f"slopes must be contiguous fp32 [{Hq}]")
+    elif not softcap:
+        return None
+    return ctypes.byref(AttnScores(softcap, _p(slopes)))
+
+
+def paged_attention_scored_into(q, k_cache, v_cache, block_table, seq_lens, out, workspace,
+                                softcap: float = 0.0, slopes=None, scale: float | None = None,
+                                window: int = 0, k_scale=None, v_scale=None) -> None:
+    """paged_attention_into with scores z capped (softcap > 0: softcap * tanh(z /
+    softcap)), then biased by distance (slopes fp32 [Hq]: + slopes[h] * (key -
+    token's position))."""
+    _paged_attention("nvfp4_paged_attention_scored", q,
+                     lambda: _kv_cache(k_cache, v_cache, k_scale, v_scale),
+                     (k_cache, v_cache, k_scale, v_scale, slopes), block_table, seq_lens, out,
+                     workspace, scale, window, _scores(softcap, slopes, q.shape[1]))
+
+
+def paged_attention_scored(q, k_cache, v_cache, block_table, seq_lens, softcap: float = 0.0,
+                           slopes=None, scale: float | None = None, window: int = 0, k_scale=None,
+                           v_scale=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    workspace, out = _attn_outputs(q, block_table, k_cache.shape[2], workspace)
+    paged_attention_scored_into(q, k_cache, v_cache, block_table, seq_lens, out, workspace,
+                                softcap, slopes, scale, window, k_scale, v_scale)
+    return out
+
+
+def paged_attention_nvfp4_into(q, k_cache, v_cache, block_table, seq_lens, out, workspace,
+                               scale: float | None = None, window: int = 0, softcap: float = 0.0,
+                               slopes=None) -> None:
+    """paged_attention_into over an NVFP4 cache (the triples of
+    rope_append_nvfp4_into), with the cap and bias of
+    paged_attention_scored_into."""
+    _paged_attention("nvfp4_paged_attention_nvfp4", q, lambda: _kv_cache4(k_cache, v_cache),
+                     (*k_cache, *v_cache, slopes), block_table, seq_lens, out, workspace, scale,
+                     window, _scores(softcap, slopes, q.shape[1]))
+
+
+def paged_attention_nvfp4(q, k_cache, v_cache, block_table, seq_lens, scale: float | None = None,
+                          window: int = 0, softcap: float = 0.0, slopes=None,
+                          workspace: torch.Tensor | None = None) -> torch.Tensor:
+    workspace, out = _attn_outputs(q, block_table, k_cache[0].shape[2], workspace)
+    paged_attention_nvfp4_into(q, k_cache, v_cache, block_table, seq_lens, out, workspace, scale,
+                               window, softcap, slopes)
+    return out
+
+
+# ------------------------------------------- beside the GEMVs: low-rank adapters
+
+def lora_workspace_bytes(M: int, K: int, rank: int, n_segments: int) -> int:
+    return int(lib().nvfp4_lora_workspace_bytes(M, K, rank, n_segments))
+
+
+def lora_segments_into(mats, x, ids, ys, workspace, bases=None, alpha=None, ranks=None) -> None:
+    """ys[s][m] = bases[s][m] + alpha[e] B_s[e] (A_s[e] x[m]) with e = ids[m], for
+    all rows m (an id outside the adapters: the base alone). mats: per projection
+    of x (bf16 [M, K]) its adapters (a bf16 [E, rank, K], b bf16 [E, N, rank]); ids
+    int32 [M]; ys fp32 [M, N]; bases: what the projections gave (fp32, ys itself
+    for in place; None: zeros); alpha fp32 [E] (None: 1); ranks int32 [E]: how
+    many of its ranks an adapter uses (None: all)."""
+    if not mats or len(ys) != len(mats) or (bases is not None and len(bases) != len(mats)):
+        raise ValueError("mats, ys and bases must have the same length, at least one")
+    bases = [None] * len(mats) if bases is None else bases
+    flat = [t for m in mats for t in m]
+    _same_device(x.get_device(), ids, workspace, alpha, ranks, *flat, *ys, *bases)
+    _contiguous(x, ids, workspace, alpha, ranks, *flat, *ys, *bases)
+    M, K = x.shape
+    E, rank, _ = mats[0][0].shape
+    if x.dtype is not torch.bfloat16 or ids.dtype is not torch.int32 \
+            or (alpha is not None and alpha.dtype is not torch.float32) \
+            or (ranks is not None and ranks.dtype is not torch.int32):
+        raise TypeError("x must be bf16, ids and ranks int32, alpha fp32")
+    if ids.shape != (M,) or (alpha is not None and alpha.shape != (E,)) \
+            or (ranks is not None and ranks.shape != (E,)):
+        raise ValueError(f"ids must be [{M}], alpha and ranks [{E}]")
+    segs = (LoraSegment * len(mats))()
+    for i, ((a, b), base, y) in enumerate(zip(mats, bases, ys)):
+        if a.dtype is not torch.bfloat16 or b.dtype is not torch.bfloat16 \
+                or y.dtype is not torch.float32 \
+                or (base is not None and base.dtype is not torch.float32):
+            raise TypeError("a and b must be bf16, bases and ys fp32")
+        N = b.shape[1]
+        if a.shape != (E, rank, K) or b.shape != (E, N, rank) or y.shape != (M, N) \
+                or (base is not None and base.shape != (M, N)):
+            raise ValueError(f"projection {i}: a must be [{E}, {rank}, {K}], b [{E}, N, {rank}], "
+                             f"base and y [{M}, N]; got {tuple(a.shape)}, {tuple(b.shape)}, "
+                             f"{None if base is None else tuple(base.shape)}, {tuple(y.shape)}")
+        segs[i] = LoraSegment(a.data_ptr(), b.data_ptr(), _p(base), y.data_ptr(), N)
+    _check("nvfp4_lora_segments", lib().nvfp4_lora_segments(
+        segs, len(mats), E, rank, ids.data_ptr(), _p(ranks), _p(alpha), x.data_ptr(), M, K,
+        workspace.data_ptr(), workspace.nbytes, _stream(x)))
+
+
+def lora_segments(mats, x, ids, bases=None, alpha=None, ranks=None,
+                  workspace: torch.Tensor | None = None):
+    """[y_s]."""
+    if workspace is None:
+        n = lora_workspace_bytes(x.shape[0], x.shape[1], mats[0][0].shape[1], len(mats))
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=x.device)
+    ys = [torch.empty((x.shape[0], b.shape[1]), dtype=torch.float32, device=x.device)
+          for _, b in mats]
+    lora_segments_into(mats, x, ids, ys, workspace, bases, alpha, ranks)
+    return ys
 
 
 # ------------------------------------------------- after the LM head: drafts

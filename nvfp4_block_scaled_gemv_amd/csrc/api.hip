@@ -508,6 +508,8 @@ nvfp4_status nvfp4_add_rmsnorm_nvfp4(const void* x, int x_type, const void* resi
   return hip_result(nvfp4::launch_add_rmsnorm(a, stream), "nvfp4_add_rmsnorm_nvfp4 launch");
 }
 
+}  // extern "C"
+
 namespace {
 
 // Bytes from a cache's first to past its last element (0: none).
@@ -551,16 +553,124 @@ nvfp4_status cache_checks(const char* fn, const nvfp4_kv_cache& c) {
   return NVFP4_OK;
 }
 
-}  // namespace
+nvfp4_status cache4_checks(const char* fn, const nvfp4_kv_cache4& c) {
+  const int64_t cb = c.D / 2, sb = c.D / 16;   // bytes of a head
+  if (c.num_blocks < 0 || c.page < 1 || c.n_kv_heads < 1 || c.D < 1 || c.D % 64 ||
+      c.stride_block < cb || c.stride_token < cb || c.stride_head < cb || c.stride_block % 16 ||
+      c.stride_token % 16 || c.stride_head % 16 || c.scale_stride_block < sb ||
+      c.scale_stride_token < sb || c.scale_stride_head < sb || c.scale_stride_block % 4 ||
+      c.scale_stride_token % 4 || c.scale_stride_head % 4)
+    return fail(NVFP4_ERR_SHAPE,
+                "%s: cache num_blocks=%lld page=%lld heads=%lld D=%lld: need num_blocks >= 0, the "
+                "others >= 1, D %% 64 == 0, strides of the codes (%lld, %lld, %lld) >= D / 2, "
+                "multiples of 16, and of the scales (%lld, %lld, %lld) >= D / 16, multiples of 4",
+                fn, (long long)c.num_blocks, (long long)c.page, (long long)c.n_kv_heads,
+                (long long)c.D, (long long)c.stride_block, (long long)c.stride_token,
+                (long long)c.stride_head, (long long)c.scale_stride_block,
+                (long long)c.scale_stride_token, (long long)c.scale_stride_head);
+  const int64_t far = 1LL << 40;
+  if (c.num_blocks > 0x7FFFFFFF || c.page > (1 << 20) || c.n_kv_heads > NVFP4_MAX_HEADS ||
+      c.D > NVFP4_ROPE_MAX_D || c.stride_token >= (1 << 26) ||
+      c.scale_stride_token >= (1 << 26) || c.stride_head >= far || c.stride_block >= far ||
+      c.scale_stride_head >= far || c.scale_stride_block >= far ||
+      (__int128)c.num_blocks * c.stride_block >= (1LL << 58) ||
+      (__int128)c.num_blocks * c.scale_stride_block >= (1LL << 58))
+    return fail(NVFP4_ERR_UNSUPPORTED,
+                "%s: cache num_blocks=%lld page=%lld heads=%lld D=%lld or a stride is past a limit",
+                fn, (long long)c.num_blocks, (long long)c.page, (long long)c.n_kv_heads,
+                (long long)c.D);
+  // the tensor scales are read also where there is no page
+  if (!c.k_gscale || !c.v_gscale)
+    return fail(NVFP4_ERR_NULL, "%s: the cache's k_gscale or v_gscale is NULL", fn);
+  if (!aligned(c.k_gscale, 4) || !aligned(c.v_gscale, 4))
+    return fail(NVFP4_ERR_ALIGN, "%s: k_gscale and v_gscale must be 4-byte aligned", fn);
+  if (c.num_blocks == 0) return NVFP4_OK;
+  if (!c.k || !c.v || !c.k_scales || !c.v_scales || c.k == c.v || c.k_scales == c.v_scales)
+    return fail(NVFP4_ERR_NULL,
+                "%s: the cache's codes and scales must be non-NULL, and differ for k and v", fn);
+  if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.k_scales, 4) ||
+      !aligned(c.v_scales, 4))
+    return fail(NVFP4_ERR_ALIGN,
+                "%s: the cache's codes must be 16-byte, its scales 4-byte aligned", fn);
+  return NVFP4_OK;
+}
 
-nvfp4_status nvfp4_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
-                               const void* v, int64_t v_stride, int x_type,
-                               const int64_t* positions, const int64_t* slots,
-                               const float* inv_freq, int64_t T, int64_t Hq, int64_t D,
-                               int64_t R, int interleaved, float rope_scale, uint16_t* q_out,
-                               const nvfp4_kv_cache* cache, hipStream_t stream) {
+// A cache's arrays, whatever it is held in: what a call writes or reads of it,
+// and its one or two fp32 scales.
+struct CacheArrays {
+  const void* p[4];
+  size_t n[4];
+  const float* scale[2];
+};
+CacheArrays arrays_of(const nvfp4_kv_cache& c) {
+  const size_t n = cache_bytes(c);
+  const bool scaled = c.type == NVFP4_E4M3;
+  return {{c.k, c.v, nullptr, nullptr},
+          {n, n, 0, 0},
+          {scaled ? c.k_scale : nullptr, scaled ? c.v_scale : nullptr}};
+}
+CacheArrays arrays_of(const nvfp4_kv_cache4& c) {
+  size_t nc = 0, ns = 0;
+  if (c.num_blocks) {
+    nc = (size_t)((c.num_blocks - 1) * c.stride_block + (c.page - 1) * c.stride_token +
+                  (c.n_kv_heads - 1) * c.stride_head + c.D / 2);
+    ns = (size_t)((c.num_blocks - 1) * c.scale_stride_block + (c.page - 1) * c.scale_stride_token +
+                  (c.n_kv_heads - 1) * c.scale_stride_head + c.D / 16);
+  }
+  return {{c.k, c.v, c.k_scales, c.v_scales}, {nc, nc, ns, ns}, {c.k_gscale, c.v_gscale}};
+}
+// [p, p + n) meets one of the arrays or scales.
+bool overlap(const void* p, size_t n, const CacheArrays& c) {
+  for (int i = 0; i < 4; ++i)
+    if (overlap(p, n, c.p[i], c.n[i])) return true;
+  return overlap(p, n, c.scale[0], 4) || overlap(p, n, c.scale[1], 4);
+}
+
+// What RopeArgs and AttnArgs hold of a cache.
+template <class Args>
+void put_cache(Args& a, const nvfp4_kv_cache& c) {
+  a.cache_e4m3 = c.type == NVFP4_E4M3;
+  a.k_cache = c.k;
+  a.v_cache = c.v;
+  a.num_blocks = c.num_blocks;
+  a.page = c.page;
+  a.Hkv = c.n_kv_heads;
+  a.sb = c.stride_block;
+  a.st = c.stride_token;
+  a.sh = c.stride_head;
+  a.k_scale = a.cache_e4m3 ? c.k_scale : nullptr;
+  a.v_scale = a.cache_e4m3 ? c.v_scale : nullptr;
+}
+template <class Args>
+void put_cache(Args& a, const nvfp4_kv_cache4& c) {
+  a.cache_nvfp4 = true;
+  a.k_cache = c.k;
+  a.v_cache = c.v;
+  a.k_blocks = c.k_scales;
+  a.v_blocks = c.v_scales;
+  a.num_blocks = c.num_blocks;
+  a.page = c.page;
+  a.Hkv = c.n_kv_heads;
+  a.sb = c.stride_block;
+  a.st = c.stride_token;
+  a.sh = c.stride_head;
+  a.block_sb = c.scale_stride_block;
+  a.block_st = c.scale_stride_token;
+  a.block_sh = c.scale_stride_head;
+  a.k_scale = c.k_gscale;
+  a.v_scale = c.v_gscale;
+}
+nvfp4_status checks_of(const char* fn, const nvfp4_kv_cache& c) { return cache_checks(fn, c); }
+nvfp4_status checks_of(const char* fn, const nvfp4_kv_cache4& c) { return cache4_checks(fn, c); }
+
+template <class Cache>
+nvfp4_status rope_checked(const char* fn, const void* q, int64_t q_stride, const void* k,
+                          int64_t k_stride, const void* v, int64_t v_stride, int x_type,
+                          const int64_t* positions, const int64_t* slots, const float* inv_freq,
+                          int64_t T, int64_t Hq, int64_t D, int64_t R, int interleaved,
+                          float rope_scale, uint16_t* q_out, const Cache* cache,
+                          hipStream_t stream) {
   clear_error();
-  const char* fn = "nvfp4_rope_append";
   if (T < 0 || Hq < 0 || D < 16 || D % 16 || R < 0 || R > D || R % 16)
     return fail(NVFP4_ERR_SHAPE,
                 "%s: need T, Hq >= 0, D >= 16, 0 <= R <= D, D and R multiples of 16 (T=%lld "
@@ -578,7 +688,7 @@ nvfp4_status nvfp4_rope_append(const void* q, int64_t q_stride, const void* k, i
                 NVFP4_ROPE_MAX_D);
   int64_t Hkv = 0;
   if (cache) {
-    const nvfp4_status st = cache_checks(fn, *cache);
+    const nvfp4_status st = checks_of(fn, *cache);
     if (st != NVFP4_OK) return st;
     Hkv = cache->n_kv_heads;
     if (cache->D != D)
@@ -609,20 +719,19 @@ nvfp4_status nvfp4_rope_append(const void* q, int64_t q_stride, const void* k, i
   const size_t kb = Hkv ? ((size_t)(T - 1) * k_stride + Hkv * D) * es : 0;
   const size_t vb = Hkv ? ((size_t)(T - 1) * v_stride + Hkv * D) * es : 0;
   const size_t ob = (size_t)T * Hq * D * 2, tb = (size_t)T * 8, fb = (size_t)R * 2;
-  const size_t cb = cache ? cache_bytes(*cache) : 0;
-  const void* outs[3] = {Hq ? q_out : nullptr, cache ? cache->k : nullptr,
-                         cache ? cache->v : nullptr};
-  const size_t obytes[3] = {ob, cb, cb};
-  const bool scaled = cache && cache->type == NVFP4_E4M3;
-  for (int i = 0; i < 3; ++i) {
+  const CacheArrays none = {};
+  const CacheArrays ca = cache ? arrays_of(*cache) : none;
+  const void* outs[5] = {Hq ? q_out : nullptr, ca.p[0], ca.p[1], ca.p[2], ca.p[3]};
+  const size_t obytes[5] = {ob, ca.n[0], ca.n[1], ca.n[2], ca.n[3]};
+  for (int i = 0; i < 5; ++i) {
     const void* o = outs[i];
     const size_t n = obytes[i];
     if ((Hq && overlap(o, n, q, qb)) || (Hkv && overlap(o, n, k, kb)) ||
         (Hkv && overlap(o, n, v, vb)) || overlap(o, n, positions, tb) ||
         (Hkv && overlap(o, n, slots, tb)) || overlap(o, n, inv_freq, fb) ||
-        (scaled && (overlap(o, n, cache->k_scale, 4) || overlap(o, n, cache->v_scale, 4))))
+        overlap(o, n, ca.scale[0], 4) || overlap(o, n, ca.scale[1], 4))
       return fail(NVFP4_ERR_ALIAS, "%s: an output overlaps an input", fn);
-    // k and v may lie in each other's gaps; q_out may not lie in theirs
+    // the cache's arrays may lie in each other's gaps; q_out may not lie in theirs
     if (i > 0 && overlap(o, n, outs[0], ob))
       return fail(NVFP4_ERR_ALIAS, "%s: q_out overlaps the cache", fn);
   }
@@ -638,7 +747,6 @@ nvfp4_status nvfp4_rope_append(const void* q, int64_t q_stride, const void* k, i
   a.inv_freq = inv_freq;
   a.T = T;
   a.Hq = Hq;
-  a.Hkv = Hkv;
   a.D = D;
   a.R = R;
   a.rope_scale = rope_scale;
@@ -646,21 +754,45 @@ nvfp4_status nvfp4_rope_append(const void* q, int64_t q_stride, const void* k, i
   a.interleaved = interleaved != 0;
   a.q_out = q_out;
   if (cache) {
-    a.cache_e4m3 = scaled;
-    a.k_cache = cache->k;
-    a.v_cache = cache->v;
-    a.num_blocks = cache->num_blocks;
-    a.page = cache->page;
-    a.sb = cache->stride_block;
-    a.st = cache->stride_token;
-    a.sh = cache->stride_head;
-    a.k_scale = cache->k_scale;
-    a.v_scale = cache->v_scale;
+    put_cache(a, *cache);
   } else {
     a.page = 1;
   }
-  return hip_result(nvfp4::launch_rope_append(a, stream), "nvfp4_rope_append launch");
+  return hip_result(nvfp4::launch_rope_append(a, stream), fn);
 }
+
+}  // namespace
+
+extern "C" {
+
+nvfp4_status nvfp4_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                               const void* v, int64_t v_stride, int x_type,
+                               const int64_t* positions, const int64_t* slots,
+                               const float* inv_freq, int64_t T, int64_t Hq, int64_t D,
+                               int64_t R, int interleaved, float rope_scale, uint16_t* q_out,
+                               const nvfp4_kv_cache* cache, hipStream_t stream) {
+  return rope_checked("nvfp4_rope_append", q, q_stride, k, k_stride, v, v_stride, x_type,
+                      positions, slots, inv_freq, T, Hq, D, R, interleaved, rope_scale, q_out,
+                      cache, stream);
+}
+
+nvfp4_status nvfp4_rope_append_nvfp4(const void* q, int64_t q_stride, const void* k,
+                                     int64_t k_stride, const void* v, int64_t v_stride,
+                                     int x_type, const int64_t* positions, const int64_t* slots,
+                                     const float* inv_freq, int64_t T, int64_t Hq, int64_t D,
+                                     int64_t R, int interleaved, float rope_scale,
+                                     uint16_t* q_out, const nvfp4_kv_cache4* cache,
+                                     hipStream_t stream) {
+  const char* fn = "nvfp4_rope_append_nvfp4";
+  if (!cache) {
+    clear_error();
+    return fail(NVFP4_ERR_NULL, "%s: cache is NULL", fn);
+  }
+  return rope_checked(fn, q, q_stride, k, k_stride, v, v_stride, x_type, positions, slots,
+                      inv_freq, T, Hq, D, R, interleaved, rope_scale, q_out, cache, stream);
+}
+
+}  // extern "C"
 
 namespace {
 
@@ -669,7 +801,89 @@ bool attn_sizes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv, int64_t D) {
          Q <= NVFP4_ATTN_MAX_Q && Hq <= NVFP4_MAX_HEADS && (D == 64 || D == 128 || D == 256);
 }
 
+template <class Cache>
+nvfp4_status attn_checked(const char* fn, const uint16_t* q, const Cache* cache,
+                          const int32_t* block_table, const int32_t* seq_lens, int64_t B,
+                          int64_t Q, int64_t Hq, int64_t max_blocks, float scale, int64_t window,
+                          const nvfp4_attn_scores* scores, uint16_t* out, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream) {
+  clear_error();
+  if (!cache) return fail(NVFP4_ERR_NULL, "%s: cache is NULL", fn);
+  const nvfp4_status st = checks_of(fn, *cache);
+  if (st != NVFP4_OK) return st;
+  const int64_t Hkv = cache->n_kv_heads, D = cache->D;
+  if (B < 0 || Q < 0 || Hq < 0 || Hq % Hkv || max_blocks < 0 || window < 0)
+    return fail(NVFP4_ERR_SHAPE,
+                "%s: need B, Q, max_blocks, window >= 0 and Hq a multiple of the cache's heads "
+                "(B=%lld Q=%lld Hq=%lld Hkv=%lld)", fn, (long long)B, (long long)Q,
+                (long long)Hq, (long long)Hkv);
+  if (!(scale > -3.0e38f && scale < 3.0e38f))
+    return fail(NVFP4_ERR_SHAPE, "%s: scale must be finite", fn);
+  const float softcap = scores ? scores->softcap : 0.0f;
+  const float* slopes = scores ? scores->slopes : nullptr;
+  if (!(softcap == 0.0f || (softcap >= 1e-6f && softcap <= 1e30f)))
+    return fail(NVFP4_ERR_SHAPE, "%s: softcap must be 0 (none) or 1e-6 .. 1e30", fn);
+  if (!attn_sizes(B, Q, Hq, Hkv, D))
+    return fail(NVFP4_ERR_UNSUPPORTED,
+                "%s: B=%lld (max %d), Q=%lld (max %d), Hq=%lld (max %d), D=%lld (64, 128 or 256)",
+                fn, (long long)B, NVFP4_ATTN_MAX_B, (long long)Q, NVFP4_ATTN_MAX_Q,
+                (long long)Hq, NVFP4_MAX_HEADS, (long long)D);
+  if (max_blocks > 0x7FFFFFFF || window > 0x7FFFFFFF)
+    return fail(NVFP4_ERR_UNSUPPORTED, "%s: max_blocks=%lld or window=%lld is past 2^31 - 1", fn,
+                (long long)max_blocks, (long long)window);
+  if (B == 0 || Q == 0 || Hq == 0) return NVFP4_OK;
+  nvfp4::AttnArgs a = {};
+  put_cache(a, *cache);
+  a.B = B;
+  a.Q = Q;
+  a.Hq = Hq;
+  a.D = D;
+  a.max_blocks = max_blocks;
+  a.window = window;
+  if (!nvfp4::attn_fits(a))
+    return fail(NVFP4_ERR_UNSUPPORTED,
+                "%s: more than 2^31 tiles of 32 keys (B * max_blocks * page), or than 2^22 "
+                "sequences times row tiles of all heads", fn);
+  if (!q || !seq_lens || !out || (max_blocks && !block_table))
+    return fail(NVFP4_ERR_NULL, "%s: NULL pointer", fn);
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(slopes, 4))
+    return fail(NVFP4_ERR_ALIGN,
+                "%s: q and out must be 16-byte, block_table, seq_lens and slopes 4-byte aligned",
+                fn);
+  const size_t need = nvfp4::attn_workspace_bytes(B, Q, Hq, Hkv, D);
+  if (!workspace || workspace_bytes < need)
+    return fail(NVFP4_ERR_WORKSPACE, "%s: the workspace needs %zu bytes, %zu given", fn, need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (!aligned(workspace, 256))
+    return fail(NVFP4_ERR_ALIGN, "%s: the workspace must be 256-byte aligned", fn);
+  const size_t qb = (size_t)B * Q * Hq * D * 2;
+  const size_t tb = (size_t)B * max_blocks * 4, lb = (size_t)B * 4;
+  const CacheArrays ca = arrays_of(*cache);
+  const void* outs[2] = {out, workspace};
+  const size_t ob[2] = {qb, need};
+  for (int i = 0; i < 2; ++i)
+    if (overlap(outs[i], ob[i], q, qb) || overlap(outs[i], ob[i], ca) ||
+        overlap(outs[i], ob[i], block_table, tb) || overlap(outs[i], ob[i], seq_lens, lb) ||
+        overlap(outs[i], ob[i], slopes, (size_t)Hq * 4))
+      return fail(NVFP4_ERR_ALIAS, "%s: the output or the workspace overlaps an input", fn);
+  if (overlap(out, qb, workspace, need))
+    return fail(NVFP4_ERR_ALIAS, "%s: the output and the workspace overlap", fn);
+  a.q = q;
+  a.table = block_table;
+  a.lens = seq_lens;
+  a.scale = scale;
+  a.softcap = softcap;
+  a.slopes = slopes;
+  a.out = out;
+  a.workspace = workspace;
+  return hip_result(a.cache_nvfp4 ? nvfp4::launch_paged_attention4(a, stream)
+                                  : nvfp4::launch_paged_attention(a, stream), fn);
+}
+
 }  // namespace
+
+extern "C" {
 
 size_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv,
                                              int64_t D) {
@@ -682,81 +896,135 @@ nvfp4_status nvfp4_paged_attention(const uint16_t* q, const nvfp4_kv_cache* cach
                                    int64_t B, int64_t Q, int64_t Hq, int64_t max_blocks,
                                    float scale, int64_t window, uint16_t* out, void* workspace,
                                    size_t workspace_bytes, hipStream_t stream) {
+  return attn_checked("nvfp4_paged_attention", q, cache, block_table, seq_lens, B, Q, Hq,
+                      max_blocks, scale, window, nullptr, out, workspace, workspace_bytes, stream);
+}
+
+nvfp4_status nvfp4_paged_attention_scored(const uint16_t* q, const nvfp4_kv_cache* cache,
+                                          const int32_t* block_table, const int32_t* seq_lens,
+                                          int64_t B, int64_t Q, int64_t Hq, int64_t max_blocks,
+                                          float scale, int64_t window,
+                                          const nvfp4_attn_scores* scores, uint16_t* out,
+                                          void* workspace, size_t workspace_bytes,
+                                          hipStream_t stream) {
+  return attn_checked("nvfp4_paged_attention_scored", q, cache, block_table, seq_lens, B, Q, Hq,
+                      max_blocks, scale, window, scores, out, workspace, workspace_bytes, stream);
+}
+
+nvfp4_status nvfp4_paged_attention_nvfp4(const uint16_t* q, const nvfp4_kv_cache4* cache,
+                                         const int32_t* block_table, const int32_t* seq_lens,
+                                         int64_t B, int64_t Q, int64_t Hq, int64_t max_blocks,
+                                         float scale, int64_t window,
+                                         const nvfp4_attn_scores* scores, uint16_t* out,
+                                         void* workspace, size_t workspace_bytes,
+                                         hipStream_t stream) {
+  return attn_checked("nvfp4_paged_attention_nvfp4", q, cache, block_table, seq_lens, B, Q, Hq,
+                      max_blocks, scale, window, scores, out, workspace, workspace_bytes, stream);
+}
+
+namespace {
+
+bool lora_sizes(int64_t M, int64_t K, int64_t rank, int64_t n_segments) {
+  return M >= 0 && K >= 0 && K % 32 == 0 && rank >= 8 && rank % 8 == 0 && n_segments >= 0;
+}
+bool lora_limits(int64_t M, int64_t K, int64_t rank, int64_t n_segments) {
+  return M <= NVFP4_MAX_M && K <= NVFP4_MAX_K && rank <= NVFP4_LORA_MAX_RANK &&
+         n_segments <= NVFP4_MAX_SEGMENTS;
+}
+
+}  // namespace
+
+size_t nvfp4_lora_workspace_bytes(int64_t M, int64_t K, int64_t rank, int64_t n_segments) {
+  if (!lora_sizes(M, K, rank, n_segments) || !lora_limits(M, K, rank, n_segments)) return 0;
+  return nvfp4::lora_workspace_bytes(M, K, rank, n_segments);
+}
+
+nvfp4_status nvfp4_lora_segments(const nvfp4_lora_segment* segs, int64_t n_segments,
+                                 int64_t n_adapters, int64_t rank, const int32_t* ids,
+                                 const int32_t* ranks, const float* alpha, const uint16_t* x,
+                                 int64_t M, int64_t K, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream) {
   clear_error();
-  const char* fn = "nvfp4_paged_attention";
-  if (!cache) return fail(NVFP4_ERR_NULL, "%s: cache is NULL", fn);
-  const nvfp4_status st = cache_checks(fn, *cache);
-  if (st != NVFP4_OK) return st;
-  const int64_t Hkv = cache->n_kv_heads, D = cache->D;
-  if (B < 0 || Q < 0 || Hq < 0 || Hq % Hkv || max_blocks < 0 || window < 0)
+  const char* fn = "nvfp4_lora_segments";
+  if (!lora_sizes(M, K, rank, n_segments) || n_adapters < 0)
     return fail(NVFP4_ERR_SHAPE,
-                "%s: need B, Q, max_blocks, window >= 0 and Hq a multiple of the cache's heads "
-                "(B=%lld Q=%lld Hq=%lld Hkv=%lld)", fn, (long long)B, (long long)Q,
-                (long long)Hq, (long long)Hkv);
-  if (!(scale > -3.0e38f && scale < 3.0e38f))
-    return fail(NVFP4_ERR_SHAPE, "%s: scale must be finite", fn);
-  if (!attn_sizes(B, Q, Hq, Hkv, D))
+                "%s: need n_segments, n_adapters, M, K >= 0, K %% 32 == 0, rank >= 8 and rank %% 8 "
+                "== 0 (n=%lld adapters=%lld rank=%lld M=%lld K=%lld)", fn, (long long)n_segments,
+                (long long)n_adapters, (long long)rank, (long long)M, (long long)K);
+  if (!lora_limits(M, K, rank, n_segments) || n_adapters > NVFP4_LORA_MAX_ADAPTERS)
     return fail(NVFP4_ERR_UNSUPPORTED,
-                "%s: B=%lld (max %d), Q=%lld (max %d), Hq=%lld (max %d), D=%lld (64, 128 or 256)",
-                fn, (long long)B, NVFP4_ATTN_MAX_B, (long long)Q, NVFP4_ATTN_MAX_Q,
-                (long long)Hq, NVFP4_MAX_HEADS, (long long)D);
-  if (max_blocks > 0x7FFFFFFF || window > 0x7FFFFFFF)
-    return fail(NVFP4_ERR_UNSUPPORTED, "%s: max_blocks=%lld or window=%lld is past 2^31 - 1", fn,
-                (long long)max_blocks, (long long)window);
-  if (B == 0 || Q == 0 || Hq == 0) return NVFP4_OK;
-  nvfp4::AttnArgs a = {};
-  a.k_cache = cache->k;
-  a.v_cache = cache->v;
-  a.num_blocks = cache->num_blocks;
-  a.page = cache->page;
-  a.sb = cache->stride_block;
-  a.st = cache->stride_token;
-  a.sh = cache->stride_head;
-  a.cache_e4m3 = cache->type == NVFP4_E4M3;
-  a.k_scale = cache->k_scale;
-  a.v_scale = cache->v_scale;
-  a.B = B;
-  a.Q = Q;
-  a.Hq = Hq;
-  a.Hkv = Hkv;
-  a.D = D;
-  a.max_blocks = max_blocks;
-  a.window = window;
-  if (!nvfp4::attn_fits(a))
-    return fail(NVFP4_ERR_UNSUPPORTED,
-                "%s: more than 2^31 tiles of 32 keys (B * max_blocks * page), or than 2^22 "
-                "sequences times row tiles of all heads", fn);
-  if (!q || !seq_lens || !out || (max_blocks && !block_table))
-    return fail(NVFP4_ERR_NULL, "%s: NULL pointer", fn);
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
-    return fail(NVFP4_ERR_ALIGN,
-                "%s: q and out must be 16-byte, block_table and seq_lens 4-byte aligned", fn);
-  const size_t need = nvfp4::attn_workspace_bytes(B, Q, Hq, Hkv, D);
-  if (!workspace || workspace_bytes < need)
+                "%s: n_segments=%lld (max %d), n_adapters=%lld (max %d), rank=%lld (max %d), "
+                "M=%lld (max %d), K=%lld (max %lld)", fn, (long long)n_segments,
+                NVFP4_MAX_SEGMENTS, (long long)n_adapters, NVFP4_LORA_MAX_ADAPTERS,
+                (long long)rank, NVFP4_LORA_MAX_RANK, (long long)M, NVFP4_MAX_M, (long long)K,
+                (long long)NVFP4_MAX_K);
+  if (n_segments == 0 || M == 0) return NVFP4_OK;
+  if (!segs) return fail(NVFP4_ERR_NULL, "%s: segs is NULL", fn);
+  nvfp4::LoraArgs a = {};
+  int64_t total_n = 0;
+  for (int64_t i = 0; i < n_segments; ++i) {
+    const nvfp4_lora_segment& g = segs[i];
+    if (g.N < 0)
+      return fail(NVFP4_ERR_SHAPE, "%s: segment %lld has N=%lld < 0", fn, (long long)i,
+                  (long long)g.N);
+    if (g.N > NVFP4_MAX_N - total_n)
+      return fail(NVFP4_ERR_UNSUPPORTED, "%s: the segments' N exceed %lld", fn,
+                  (long long)NVFP4_MAX_N);
+    total_n += g.N;
+    if (g.N == 0) continue;
+    if (!g.y || (n_adapters && (!g.b || (K && !g.a))))
+      return fail(NVFP4_ERR_NULL, "%s: segment %lld has a NULL pointer", fn, (long long)i);
+    if (!aligned(g.a, 16) || !aligned(g.b, 16) || !aligned(g.y, 4) || !aligned(g.base, 4))
+      return fail(NVFP4_ERR_ALIGN,
+                  "%s: segment %lld: a and b must be 16-byte, base and y 4-byte aligned", fn,
+                  (long long)i);
+    nvfp4::LoraSegment& d = a.segs[a.n_segments++];
+    d.a = g.a;
+    d.b = g.b;
+    d.base = g.base;
+    d.y = g.y;
+    d.N = g.N;
+  }
+  if (a.n_segments == 0) return NVFP4_OK;
+  if (!ids || (K && !x)) return fail(NVFP4_ERR_NULL, "%s: ids or x is NULL", fn);
+  if (!aligned(ids, 4) || !aligned(ranks, 4) || !aligned(alpha, 4) || !aligned(x, 16))
+    return fail(NVFP4_ERR_ALIGN, "%s: x must be 16-byte, ids, ranks and alpha 4-byte aligned", fn);
+  const size_t need = nvfp4::lora_workspace_bytes(M, K, rank, n_segments);
+  if (need && (!workspace || workspace_bytes < need))
     return fail(NVFP4_ERR_WORKSPACE, "%s: the workspace needs %zu bytes, %zu given", fn, need,
                 workspace ? workspace_bytes : (size_t)0);
-  if (!aligned(workspace, 256))
+  if (need && !aligned(workspace, 256))
     return fail(NVFP4_ERR_ALIGN, "%s: the workspace must be 256-byte aligned", fn);
-  const size_t qb = (size_t)B * Q * Hq * D * 2, cb = cache_bytes(*cache);
-  const size_t tb = (size_t)B * max_blocks * 4, lb = (size_t)B * 4;
-  const void* outs[2] = {out, workspace};
-  const size_t ob[2] = {qb, need};
-  for (int i = 0; i < 2; ++i)
-    if (overlap(outs[i], ob[i], q, qb) || overlap(outs[i], ob[i], cache->k, cb) ||
-        overlap(outs[i], ob[i], cache->v, cb) || overlap(outs[i], ob[i], block_table, tb) ||
-        overlap(outs[i], ob[i], seq_lens, lb) ||
-        (cache->type == NVFP4_E4M3 && (overlap(outs[i], ob[i], cache->k_scale, 4) ||
-                                       overlap(outs[i], ob[i], cache->v_scale, 4))))
-      return fail(NVFP4_ERR_ALIAS, "%s: the output or the workspace overlaps an input", fn);
-  if (overlap(out, qb, workspace, need))
-    return fail(NVFP4_ERR_ALIAS, "%s: the output and the workspace overlap", fn);
-  a.q = q;
-  a.table = block_table;
-  a.lens = seq_lens;
-  a.scale = scale;
-  a.out = out;
+  const size_t xb = (size_t)M * K * 2, eb = (size_t)n_adapters * 4;
+  for (int i = 0; i <= a.n_segments; ++i) {
+    const bool ws = i == a.n_segments;   // the workspace, after the outputs
+    const void* o = ws ? workspace : a.segs[i].y;
+    const size_t n = ws ? need : (size_t)M * a.segs[i].N * 4;
+    if (overlap(o, n, ids, (size_t)M * 4) || overlap(o, n, ranks, eb) ||
+        overlap(o, n, alpha, eb) || overlap(o, n, x, xb))
+      return fail(NVFP4_ERR_ALIAS, "%s: an output or the workspace overlaps an input", fn);
+    for (int j = 0; j < a.n_segments; ++j) {
+      const nvfp4::LoraSegment& g = a.segs[j];
+      const size_t yb = (size_t)M * g.N * 4;
+      const bool in_place = i == j && g.base == g.y;
+      if (overlap(o, n, g.a, (size_t)n_adapters * rank * K * 2) ||
+          overlap(o, n, g.b, (size_t)n_adapters * rank * g.N * 2) ||
+          (!in_place && overlap(o, n, g.base, yb)))
+        return fail(NVFP4_ERR_ALIAS, "%s: an output or the workspace overlaps an input", fn);
+      if (i != j && overlap(o, n, g.y, yb))
+        return fail(NVFP4_ERR_ALIAS, "%s: two outputs, or one and the workspace, overlap", fn);
+    }
+  }
+  a.x = x;
+  a.ids = ids;
+  a.ranks = ranks;
+  a.alpha = alpha;
+  a.n_adapters = n_adapters;
+  a.rank = rank;
+  a.M = M;
+  a.K = K;
   a.workspace = workspace;
-  return hip_result(nvfp4::launch_paged_attention(a, stream), "nvfp4_paged_attention launch");
+  return hip_result(nvfp4::launch_lora(a, stream), "nvfp4_lora_segments launch");
 }
 
 namespace {

@@ -1,0 +1,620 @@
+// attn_wave.h -- what attention over a paged cache shares whatever its cache is
+// held in: the split of the work, a wavefront's pass over tiles of keys, the
+// scores' cap and bias, the two forms' kernels and the join of partial sums.
+// The caches' own parts (paged_attn.hip: bf16 and E4M3, paged_attn4.hip: NVFP4)
+// are classes derived from AttnPass.
+#pragma once
+
+#include "elems.h"
+#include "attn_span.h"
+#include "internal.h"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kCus = 256;
+constexpr int kWholeWaves = 8;   // wavefronts per workgroup of the whole form
+constexpr float kLog2e = 1.4426950408889634f;
+// s_waitcnt vmcnt(0), no other counter.
+constexpr int kVmcnt0 = 0x0F70;
+// Runs of one head at most: all its wavefronts on the chip, where there is but
+// one head (the layouts).
+constexpr int kMaxRuns = kCus * 4 * 2;
+
+struct AttnShape {
+  int rows;        // G * Q
+  int G;
+  int NHV;         // heads as the wavefronts see them: Hkv * row tiles
+  int groups;      // runs
+  int page_shift;  // log2(page), or -1
+  int cap;         // keys that a row of the table can name
+  int slot_rows;   // rows of one partial record
+  float* ml;       // [slots][slot_rows][2]
+  float* o;        // [slots][slot_rows][D]
+};
+
+typedef const __attribute__((address_space(4))) int32_t* const_i32;
+
+__device__ __forceinline__ Span span_of(const AttnArgs& a, const AttnShape& sh, int len) {
+  return nvfp4::span_of(len, sh.cap, a.Q, a.window);
+}
+
+// Inclusive sums over the 64 lanes, by DPP: within rows of 16, then from each
+// row's last lane to the rows after it.
+__device__ __forceinline__ int scan64(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);   // row_shr:2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);   // row_shr:4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);   // row_shr:8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, true);   // row_bcast:15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, true);   // row_bcast:31
+  return v;
+}
+
+// The tiles of all sequences, by every wavefront for itself (all 64 lanes).
+struct Tiles {
+  const AttnArgs& a;
+  const AttnShape& sh;
+  const int lane;
+  int len, n, incl;   // of sequence `lane`, and the tiles up to it (of the first 64)
+  int total;
+  __device__ __forceinline__ Tiles(const AttnArgs& a_, const AttnShape& sh_)
+      : a(a_), sh(sh_), lane(threadIdx.x & 63) {
+    len = lane < (int)a.B ? a.lens[lane] : 0;
+    n = lane < (int)a.B ? span_of(a, sh, len).n : 0;
+    incl = scan64(n);
+    total = __builtin_amdgcn_readlane(incl, 63);
+    for (int b0 = 64; b0 < (int)a.B; b0 += 64) {
+      const int b = b0 + lane;
+      const int m = b < (int)a.B ? span_of(a, sh, a.lens[b]).n : 0;
+      total += __builtin_amdgcn_readlane(scan64(m), 63);
+    }
+  }
+  // The sequence that holds tile u, its length, and the tiles before it.
+  __device__ __forceinline__ int find(int u, int& before, int& its_len) const {
+    int run = 0, len_l = len, n_l = n, incl_l = incl;
+    for (int b0 = 0;;) {
+      const uint64_t past = __ballot(run + incl_l > u);
+      if (past) {
+        const int l = __builtin_ctzll(past);
+        before = run + __builtin_amdgcn_readlane(incl_l - n_l, l);
+        its_len = __builtin_amdgcn_readlane(len_l, l);
+        return b0 + l;
+      }
+      run += __builtin_amdgcn_readlane(incl_l, 63);
+      b0 += 64;
+      if (b0 >= (int)a.B) break;   // not reached for u below the total
+      len_l = b0 + lane < (int)a.B ? a.lens[b0 + lane] : 0;
+      n_l = b0 + lane < (int)a.B ? span_of(a, sh, len_l).n : 0;
+      incl_l = scan64(n_l);
+    }
+    before = its_len = 0;
+    return 0;
+  }
+  // The tiles before sequence b.
+  __device__ __forceinline__ int before(int b) const {
+    int run = 0, n_l = n, incl_l = incl;
+    for (int b0 = 0; b - b0 >= 64;) {
+      run += __builtin_amdgcn_readlane(incl_l, 63);
+      b0 += 64;
+      n_l = b0 + lane < (int)a.B ? span_of(a, sh, a.lens[b0 + lane]).n : 0;
+      incl_l = scan64(n_l);
+    }
+    return run + __builtin_amdgcn_readlane(incl_l - n_l, b & 63);
+  }
+};
+// Run w starts at tile start(w); the first r runs have q + 1 tiles and the
+// others q (nw * q + r in all). of(s): the run that has tile s.
+struct Runs {
+  int nw, q, r;
+  __device__ __forceinline__ Runs(int total, int groups) {
+    nw = total < groups ? total : groups;
+    q = total / nw;
+    r = total % nw;
+  }
+  __device__ __forceinline__ int start(int w) const { return w * q + (w < r ? w : r); }
+  __device__ __forceinline__ int of(int s) const {
+    const int big = r * (q + 1);
+    return s < big ? s / (q + 1) : r + (s - big) / q;
+  }
+};
+
+__device__ __forceinline__ uint32_t perm_lo(uint32_t a, uint32_t b) {   // halves 0 of a, b
+  return __builtin_amdgcn_perm(b, a, 0x05040100u);
+}
+__device__ __forceinline__ uint32_t perm_hi(uint32_t a, uint32_t b) {   // halves 1 of a, b
+  return __builtin_amdgcn_perm(b, a, 0x07060302u);
+}
+// tanh to 2^-22 of it: the odd series up to 0.3 (its next term is 2^-24 there),
+// then 1 - 2 / (exp(2 x) + 1), which is 1 where the exponential overflows. The
+// series takes over where the second form's rounding, 2^-24 of one, would show.
+__device__ __forceinline__ float tanh_32(float x) {
+  const float y = fabsf(x), s = x * x;
+  const float big = fmaf(-2.0f, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(y * (2.0f * kLog2e)) + 1.0f), 1.0f);
+  float p = fmaf(s, 62.0f / 2835.0f, -17.0f / 315.0f);
+  p = fmaf(s, p, 2.0f / 15.0f);
+  p = fmaf(s, p, -1.0f / 3.0f);
+  p = fmaf(s * y, p, y);
+  return copysignf(y < 0.3f ? p : big, x);
+}
+
+// A tile of a wavefront's run.
+struct Cursor {
+  int b, len;   // its sequence
+  int key;      // its first key
+  int left;     // tiles of the sequence from it on
+};
+
+// A wavefront's pass over tiles of one head, for a class W derived from it that
+// holds K and V of a tile and the sums O. NU = TK / 16 runs of 16 keys make a
+// tile; RT tiles of 16 rows share it. Score e (of TK / 4) of a lane is row rt *
+// 16 + n and key W::key_of(e, g) of the tile. PG: pages hold whole runs of 16
+// keys. MOD: the scores are capped or biased.
+template <class W, int RT, bool PG, bool MOD>
+struct AttnPass {
+  static constexpr int kRT = RT;
+  static constexpr int NU = TK / 16;           // runs of 16 keys
+  static constexpr int NO = PG ? NU : 1;
+  static constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+  const AttnArgs& a;
+  const AttnShape& sh;
+  const const_i32 lens;
+  const int lane, n, g;
+  const int h, Q, G, row0, rows;
+  int len_after;                               // of the sequence after the last cursor's
+  int tok[RT];
+  const float c;                               // scale of the scores, log2 (cap: of tanh's argument)
+  float slope[RT];                             // of the row's head, log2 (MOD)
+  float m[RT], l[RT];
+  // Where a tile's keys lie. fetch() reads the page numbers, a tile ahead of
+  // resolve(), which turns them into places: PG, runs of 16 keys inside one
+  // page each (uniform); otherwise one place per lane, for key lane % TK. ok:
+  // bit per key, its page exists (page 0 is read in its place).
+  int ids[NO], in_page[NO];
+  uint32_t ok;
+
+  __device__ __forceinline__ W& self() { return *static_cast<W*>(this); }
+  __device__ __forceinline__ AttnPass(const AttnArgs& a_, const AttnShape& sh_, int h_, int row0_,
+                                      float k_scale)
+      : a(a_), sh(sh_), lens((const_i32)(uintptr_t)a_.lens), lane(threadIdx.x & 63),
+        n(lane & 15), g(lane >> 4), h(h_), Q((int)a_.Q), G(sh_.G), row0(row0_),
+        rows(sh_.rows - row0_ < RT * 16 ? sh_.rows - row0_ : RT * 16),
+        c(MOD && a_.softcap > 0.0f ? a_.scale * k_scale / a_.softcap
+                                   : a_.scale * k_scale * kLog2e) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int r = row0 + rt * 16 + n;
+      tok[rt] = r < sh.rows ? r / G : -1;
+      if (MOD) slope[rt] = a.slopes && tok[rt] >= 0 ? a.slopes[h * G + r - tok[rt] * G] * kLog2e : 0.0f;
+    }
+  }
+  __device__ __forceinline__ Cursor first_of(int b, int len, int idx) {
+    const Span s = span_of(a, sh, len);
+    len_after = lens[b + 1 < (int)a.B ? b + 1 : b];
+    return Cursor{b, s.len, s.base + idx * TK, s.n - idx};
+  }
+  // The tile `step` further in c's sequence, or the next one's first (past the
+  // last sequence: any tile, it is not computed).
+  __device__ __forceinline__ Cursor after(const Cursor& c, int step) {
+    if (c.left <= step && c.b + 1 < (int)a.B) return first_of(c.b + 1, len_after, 0);
+    return Cursor{c.b, c.len, tile_after(c.key, step), c.left - step};
+  }
+
+  __device__ __forceinline__ int page_of(int key, int ahead, int& in) const {
+    return nvfp4::page_of(key, ahead, (int)a.page, sh.page_shift, (int)a.max_blocks, in);
+  }
+  // Only for tiles that hold a key: an empty sequence's table has no row.
+  __device__ __forceinline__ void fetch(const Cursor& c) {
+    if constexpr (PG) {
+      const const_i32 table = (const_i32)(uintptr_t)(a.table + (int64_t)c.b * a.max_blocks);
+#pragma unroll
+      for (int u = 0; u < NU; ++u) ids[u] = table[page_of(c.key, 16 * u, in_page[u])];
+    } else {
+      const int pi = page_of(c.key, lane & (TK - 1), in_page[0]);
+      ids[0] = a.table[(int64_t)c.b * a.max_blocks + pi];
+    }
+  }
+  __device__ __forceinline__ void resolve() {
+    ok = 0;
+#pragma unroll
+    for (int u = 0; u < NO; ++u) {
+      const bool fine = (uint32_t)ids[u] < (uint32_t)a.num_blocks;
+      self().place(u, fine ? ids[u] : 0, in_page[u]);
+      if (PG)
+        ok |= fine ? 0xFFFFu << (16 * u) : 0u;
+      else
+        ok = (uint32_t)__ballot(fine);
+    }
+  }
+  // lane src's 64 bits
+  __device__ __forceinline__ int64_t from_lane(int64_t v, int src) const {
+    const int lo = __shfl((int)v, src, 64);
+    const int hi = __shfl((int)(v >> 32), src, 64);
+    return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
+  }
+
+  // The scores' cap, z -> cap tanh(z / cap) (the scores come divided by it), and
+  // the bias slope * (key - the row's position).
+  __device__ __forceinline__ void modify(f32x4_t (&S)[RT][NU], const Cursor& cur) {
+    if (a.softcap > 0.0f) {
+      const float to = a.softcap * kLog2e;
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int e = 0; e < 4 * NU; ++e)
+          S[rt][e >> 2][e & 3] = to * tanh_32(S[rt][e >> 2][e & 3]);
+    }
+    if (a.slopes) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const int from = cur.key - (cur.len - Q + tok[rt]);
+#pragma unroll
+        for (int e = 0; e < 4 * NU; ++e)
+          S[rt][e >> 2][e & 3] = fmaf(slope[rt], (float)(from + W::key_of(e, g)), S[rt][e >> 2][e & 3]);
+      }
+    }
+  }
+
+  // `count` (>= 1) tiles from cur on, `step` apart. While a tile is computed
+  // the next one is loaded (K while the values are multiplied, V while the
+  // next scores are), also across sequences. finish(cursor) where a
+  // sequence or the run ends, with O, m and l (summed over a row's lanes) of
+  // the tiles since the last one. One body for every kind of tile: code that
+  // runs once is paid for in instruction fetches.
+  template <typename F>
+  __device__ __forceinline__ void pass(Cursor cur, int count, int step, F finish) {
+    W& w = self();
+    w.load_q(cur.b);
+    fetch(cur);
+    resolve();
+    w.load_k(true);
+    w.load_v(true);
+    Cursor nxt = after(cur, step);
+    fetch(nxt);
+    const int t0 = row0 / G, t1 = (row0 + rows - 1) / G;   // the rows' tokens
+    for (;;) {
+      const bool more = --count > 0;
+      f32x4_t S[RT][NU];
+      typename W::Weights pf;
+      w.scores(S);
+      const uint32_t ok_now = ok;
+      resolve();
+      w.load_k(more);
+      const Cursor nxt2 = after(nxt, step);
+      fetch(nxt2);
+      if (MOD) modify(S, cur);
+      // every row sees the whole tile
+      const int pos0 = cur.len - Q;
+      const bool all = ok_now == kAll && cur.key + TK - 1 <= pos0 &&
+                       (!a.window || cur.key >= (int64_t)cur.len - a.window);
+      uint32_t weightless[RT];
+      if (!all) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const int hi = tok[rt] < 0 ? -1 : pos0 + tok[rt];
+          const int64_t lo = a.window ? (int64_t)hi - a.window + 1 : 0;
+          weightless[rt] = 0u;
+#pragma unroll
+          for (int e = 0; e < 4 * NU; ++e) {
+            const int key = cur.key + W::key_of(e, g);
+            if (key > hi || key < lo || !((ok_now >> W::key_of(e, g)) & 1u)) {
+              S[rt][e >> 2][e & 3] = -INFINITY;
+              weightless[rt] |= 1u << e;
+            }
+          }
+        }
+      }
+      w.softmax(S, pf);
+      if (!all) {
+        // Values that no row sees may be anything: they become zero.
+        const int last = cur.len - Q + t1;
+        const int64_t firsts = a.window ? (int64_t)cur.len - Q + t0 - a.window + 1 : 0;
+#pragma unroll
+        for (int e = 0; e < TK / 4; ++e) {
+          const int key = cur.key + W::key_of(e, g);
+          w.keep(e, key <= last && key >= firsts && ((ok_now >> W::key_of(e, g)) & 1u));
+        }
+        if (t1 > t0) settle(weightless);
+      }
+      w.values(pf);
+      w.load_v(more);
+      if (!more || nxt.b != cur.b) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {   // a row's four lanes (their maxima are the same)
+          l[rt] += __shfl_xor(l[rt], 16, 64);
+          l[rt] += __shfl_xor(l[rt], 32, 64);
+        }
+        finish(cur);
+        if (!more) break;
+        w.clear();
+        w.load_q(nxt.b);
+        // here, on the rare path: otherwise every tile would wait for queries
+        // that may be in flight, and with them for its successor
+        __builtin_amdgcn_s_waitcnt(kVmcnt0);
+      }
+      cur = nxt;
+      nxt = nxt2;
+    }
+  }
+  // A key that some rows see and others do not has weight 0 for these, which is
+  // enough unless its value is infinite or NaN (0 * inf would reach them). Such
+  // a value becomes zero, and the sum of the rows that see it NaN. weightless:
+  // bit e, this lane's row does not see key e.
+  __device__ __forceinline__ void settle(const uint32_t (&weightless)[RT]) {
+#pragma unroll
+    for (int e = 0; e < TK / 4; ++e) {
+      const bool bad = self().not_finite(e);
+      self().keep(e, !bad);
+      const bool any = (__ballot(bad) >> (16 * g)) & 0xFFFFu;   // of the key's 16 lanes
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        if (any && !((weightless[rt] >> e) & 1u)) l[rt] = __builtin_nanf("");
+    }
+  }
+};
+
+__device__ __forceinline__ void store4(uint16_t* p, f32x4_t v) {
+  *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+}
+
+// The split form: a wavefront per (run, head).
+template <class Wave>
+__global__ __launch_bounds__(256, Wave::kPerSimd) void k_attn_runs(const AttnArgs a,
+                                                                   const AttnShape sh) {
+  constexpr int D = Wave::kD, RT = Wave::kRT;
+  const Tiles tiles(a, sh);
+  const Runs runs(tiles.total, sh.groups);
+  const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int w = unit / sh.NHV, hv = unit - w * sh.NHV;
+  if (w >= runs.nw) return;
+  const int rt_tile = hv / (int)a.Hkv, h = hv - rt_tile * (int)a.Hkv;
+  const int s = runs.start(w), count = runs.start(w + 1) - s;
+  int before, len;
+  const int b = tiles.find(s, before, len);
+  const float ks = Wave::kScaled ? *a.k_scale : 1.0f, vs = Wave::kScaled ? *a.v_scale : 1.0f;
+  Wave wave(a, sh, h, rt_tile * (RT * 16), ks);
+  bool from_start = s == before;
+  int64_t rec = (int64_t)(w * sh.NHV + hv) * 2 * sh.slot_rows;
+  wave.pass(wave.first_of(b, len, s - before), count, 1, [&](const Cursor& c) {
+    const bool whole = from_start && c.left == 1;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      if (wave.tok[rt] < 0) continue;
+      const int r = rt * 16 + wave.n;
+      if (whole) {
+        const float f = wave.l[rt] == 0.0f ? 0.0f : vs / wave.l[rt];
+        uint16_t* o = a.out + ((int64_t)(c.b * a.Q + wave.tok[rt]) * a.Hq + h * sh.G +
+                               (wave.row0 + r - wave.tok[rt] * sh.G)) * D;
+        wave.each4(rt, [&](int d, f32x4_t v) { store4(o + d, v * f); });
+      } else {
+        if (wave.g == 0) {
+          sh.ml[(rec + r) * 2] = wave.m[rt];
+          sh.ml[(rec + r) * 2 + 1] = wave.l[rt];
+        }
+        float* o = sh.o + (rec + r) * D;
+        wave.each4(rt, [&](int d, f32x4_t v) { *reinterpret_cast<f32x4_t*>(o + d) = v; });
+      }
+    }
+    // only a run's first and last parts can be records
+    rec = ((int64_t)(w * sh.NHV + hv) * 2 + 1) * sh.slot_rows;
+    from_start = true;
+  });
+}
+
+// The whole form: a workgroup per (sequence, head); its wavefronts take the
+// tiles in turn and meet in LDS.
+template <class Wave>
+__global__ __launch_bounds__(kWholeWaves * 64, 2) void k_attn_whole(const AttnArgs a,
+                                                                    const AttnShape sh) {
+  constexpr int D = Wave::kD, RT = Wave::kRT;
+  __shared__ float lds_o[kWholeWaves][RT * 16][D + 4];
+  __shared__ float lds_ml[kWholeWaves][RT * 16][2];
+  const int b = blockIdx.x / sh.NHV, hv = blockIdx.x - b * sh.NHV;
+  const int rt_tile = hv / (int)a.Hkv, h = hv - rt_tile * (int)a.Hkv;
+  const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const float ks = Wave::kScaled ? *a.k_scale : 1.0f, vs = Wave::kScaled ? *a.v_scale : 1.0f;
+  const int len = ((const_i32)(uintptr_t)a.lens)[b];
+  Wave wave(a, sh, h, rt_tile * (RT * 16), ks);
+  const int count = (span_of(a, sh, len).n - wv + kWholeWaves - 1) / kWholeWaves;
+  if (count > 0) wave.pass(wave.first_of(b, len, wv), count, kWholeWaves, [](const Cursor&) {});
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+    if (wave.g == 0) {
+      lds_ml[wv][rt * 16 + wave.n][0] = wave.m[rt];
+      lds_ml[wv][rt * 16 + wave.n][1] = wave.l[rt];
+    }
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+    wave.each4(rt, [&](int d, f32x4_t v) {
+      *reinterpret_cast<f32x4_t*>(&lds_o[wv][rt * 16 + wave.n][d]) = v;
+    });
+  __syncthreads();
+  for (int it = threadIdx.x; it < wave.rows * (D / 8); it += kWholeWaves * 64) {
+    const int r = it / (D / 8), d0 = (it % (D / 8)) * 8;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int v = 0; v < kWholeWaves; ++v) mm = fmaxf(mm, lds_ml[v][r][0]);
+    const float m_use = mm == -INFINITY ? 0.0f : mm;
+    float ll = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+    for (int v = 0; v < kWholeWaves; ++v) {
+      const float f = __builtin_amdgcn_exp2f(lds_ml[v][r][0] - m_use);
+      ll = fmaf(lds_ml[v][r][1], f, ll);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = fmaf(lds_o[v][r][d0 + e], f, o[e]);
+    }
+    const float f = ll == 0.0f ? 0.0f : vs / ll;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= f;
+    const int rr = wave.row0 + r, t = rr / sh.G;
+    store8(a.out + ((int64_t)(b * a.Q + t) * a.Hq + h * sh.G + (rr - t * sh.G)) * D + d0, o);
+  }
+}
+
+// One workgroup per (sequence, head, row) of a sequence that several runs
+// share: the records' weights first, then groups of D / 4 threads add the
+// records in turn and meet in LDS.
+template <int D>
+__global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnShape sh) {
+  constexpr int TD = D / 4, NG = 256 / TD;
+  __shared__ float lds[NG][D + 4];
+  __shared__ float lds_f[kMaxRuns];
+  __shared__ float lds_red[2][4];
+  const int b = blockIdx.x / sh.NHV, hv = blockIdx.x % sh.NHV, r = blockIdx.y;
+  const int rt_tile = hv / (int)a.Hkv, h = hv - rt_tile * (int)a.Hkv;
+  const int rr = rt_tile * sh.slot_rows + r;
+  if (rr >= sh.rows) return;
+  const Tiles tiles(a, sh);
+  const Runs runs(tiles.total, sh.groups);
+  const int s0 = tiles.before(b), nb = span_of(a, sh, a.lens[b]).n;
+  const int lane = threadIdx.x & 63;
+  const int w0 = runs.of(s0), w1 = runs.of(s0 + nb - 1);
+  if (w0 == w1) return;   // finished by its one wavefront
+  // a run that starts inside this sequence, or with it, has it as its first
+  // part
+  const int odd = runs.start(w0) == s0 ? 0 : 1;
+  auto record = [&](int i) {
+    return (((int64_t)(w0 + i) * sh.NHV + hv) * 2 + (i == 0 ? odd : 0)) * sh.slot_rows + r;
+  };
+  const int np = w1 - w0 + 1, wv = threadIdx.x >> 6;
+  // the first records' values are on their way while the weights are made
+  constexpr int kEarly = 8;
+  const int grp = threadIdx.x / TD, d0 = (threadIdx.x % TD) * 4;
+  f32x4_t early[kEarly];
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+    if (grp + k * NG < np)
+      early[k] = *reinterpret_cast<const f32x4_t*>(sh.o + record(grp + k * NG) * D + d0);
+  // the records' weights against their largest maximum, and the sum
+  float mx = -INFINITY;
+  for (int i = threadIdx.x; i < np; i += 256) {
+    const float m = sh.ml[record(i) * 2];
+    lds_f[i] = m;
+    mx = fmaxf(mx, m);
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o, 64));
+  if (lane == 0) lds_red[0][wv] = mx;
+  __syncthreads();
+  mx = fmaxf(fmaxf(lds_red[0][0], lds_red[0][1]), fmaxf(lds_red[0][2], lds_red[0][3]));
+  const float use = mx == -INFINITY ? 0.0f : mx;
+  float l = 0.0f;
+  for (int i = threadIdx.x; i < np; i += 256) {
+    const float f = __builtin_amdgcn_exp2f(lds_f[i] - use);
+    lds_f[i] = f;
+    l = fmaf(sh.ml[record(i) * 2 + 1], f, l);
+  }
+  l = wave_sum(l);
+  if (lane == 0) lds_red[1][wv] = l;
+  __syncthreads();
+  l = (lds_red[1][0] + lds_red[1][1]) + (lds_red[1][2] + lds_red[1][3]);
+  f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto add = [&](f32x4_t ow, float f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = fmaf(ow[e], f, o[e]);
+  };
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+    if (grp + k * NG < np) add(early[k], lds_f[grp + k * NG]);
+#pragma unroll 8
+  for (int i = grp + kEarly * NG; i < np; i += NG)
+    add(*reinterpret_cast<const f32x4_t*>(sh.o + record(i) * D + d0), lds_f[i]);
+  *reinterpret_cast<f32x4_t*>(&lds[grp][d0]) = o;
+  __syncthreads();
+  if (threadIdx.x >= D / 8) return;
+  const int d = threadIdx.x * 8;
+  const float f = l == 0.0f ? 0.0f : (a.v_scale ? *a.v_scale : 1.0f) / l;
+  float out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+  for (int v = 0; v < NG; ++v)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] += lds[v][d + e];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) out[e] *= f;
+  const int t = rr / sh.G;
+  store8(a.out + ((int64_t)(b * a.Q + t) * a.Hq + h * sh.G + (rr - t * sh.G)) * D + d, out);
+}
+
+// The most runs per head (all heads' together fill the SIMDs with `per_simd`
+// wavefronts), and where their records lie in the workspace.
+struct AttnLayout {
+  size_t ml, o, total;
+  int RT, slot_rows, NHV, groups;
+};
+AttnLayout attn_layout(int64_t rows, int64_t Hkv, int64_t D, int RT, int per_simd) {
+  AttnLayout L;
+  L.RT = RT;
+  L.NHV = (int)(Hkv * ((rows + L.RT * 16 - 1) / (L.RT * 16)));
+  L.slot_rows = (int)(rows < L.RT * 16 ? rows : L.RT * 16);
+  L.groups = kCus * 4 * per_simd / L.NHV;
+  if (L.groups < 1) L.groups = 1;
+  const size_t slots = (size_t)2 * L.groups * L.NHV;
+  L.ml = 0;
+  L.o = (slots * L.slot_rows * 2 * sizeof(float) + 255) & ~(size_t)255;
+  L.total = (L.o + slots * L.slot_rows * (size_t)D * sizeof(float) + 255) & ~(size_t)255;
+  return L;
+}
+
+// Keys that a row of the table can name (none where there is no page).
+int capacity(const AttnArgs& a) {
+  const int64_t cap = a.num_blocks ? a.max_blocks * a.page : 0;
+  return (int)(cap < 0x7FFFFFFF ? cap : 0x7FFFFFFF);
+}
+// Keys that a sequence reads at most: by its table row, or by its window
+// (which starts at most a tile early).
+int64_t most_keys(const AttnArgs& a) {
+  const int64_t keys = capacity(a);
+  return a.window && a.window + a.Q + 64 < keys ? a.window + a.Q + 64 : keys;
+}
+
+AttnShape attn_shape(const AttnArgs& a, const AttnLayout& L) {
+  AttnShape sh;
+  sh.G = (int)(a.Hq / a.Hkv);
+  sh.rows = sh.G * (int)a.Q;
+  sh.NHV = L.NHV;
+  sh.groups = L.groups;
+  sh.cap = capacity(a);
+  sh.page_shift = (a.page & (a.page - 1)) == 0 ? __builtin_ctzll((uint64_t)a.page) : -1;
+  sh.slot_rows = L.slot_rows;
+  sh.ml = (float*)((char*)a.workspace + L.ml);
+  sh.o = (float*)((char*)a.workspace + L.o);
+  return sh;
+}
+
+// The whole form for tables of at most `whole` keys, else the split form and,
+// where a sequence can be shared, the join.
+template <class Wave>
+hipError_t launch_forms(const AttnArgs& a, AttnShape sh, int64_t whole, hipStream_t stream) {
+  constexpr int D = Wave::kD;
+  const int64_t keys = most_keys(a);
+  // no page at all: every sequence is empty
+  if (sh.cap == 0)
+    return launch_fill_zero((float*)a.out, (size_t)(a.B * a.Q * a.Hq * D / 2), stream);
+  // Heads of 256 have no whole form: eight wavefronts leave 256 registers each,
+  // which two row tiles of 128 fill already (4 to 53 VGPRs spill in three of the
+  // four bf16 and E4M3 forms).
+  if constexpr (D < 256) {
+    if (keys <= whole) {
+      hipLaunchKernelGGL((k_attn_whole<Wave>), dim3((uint32_t)(a.B * sh.NHV)),
+                         dim3(kWholeWaves * 64), 0, stream, a, sh);
+      return hipGetLastError();
+    }
+  }
+  const int64_t most = (keys + TK - 1) / TK * a.B;   // tiles
+  if (most < sh.groups) sh.groups = (int)most;
+  const int64_t units = (int64_t)sh.groups * sh.NHV;
+  hipLaunchKernelGGL((k_attn_runs<Wave>), dim3((uint32_t)((units + 3) / 4)), dim3(256), 0, stream,
+                     a, sh);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || keys <= TK) return e;   // a sequence of one tile is never shared
+  hipLaunchKernelGGL((k_attn_join<D>),
+                     dim3((uint32_t)(a.B * sh.NHV), (uint32_t)sh.slot_rows), dim3(256), 0, stream,
+                     a, sh);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+}  // namespace nvfp4

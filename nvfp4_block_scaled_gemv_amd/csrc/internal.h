@@ -180,11 +180,15 @@ struct RopeArgs {
   const float* inv_freq;             // [R / 2]
   int64_t T, Hq, Hkv, D, R;
   float rope_scale;
-  bool x_f32, interleaved, cache_e4m3;
+  bool x_f32, interleaved, cache_e4m3, cache_nvfp4;
   uint16_t* q_out;                   // bf16 [T, Hq, D]
   void *k_cache, *v_cache;           // [num_blocks, page, Hkv, D], strided
   int64_t num_blocks, page, sb, st, sh;   // strides in elements: block, token, head
-  const float *k_scale, *v_scale;    // E4M3 cache: float [1] each
+  const float *k_scale, *v_scale;    // E4M3, NVFP4: float [1] each
+  // NVFP4: k_cache, v_cache hold the codes and sb, st, sh count bytes; the block
+  // scales, and their strides in bytes
+  uint8_t *k_blocks, *v_blocks;
+  int64_t block_sb, block_st, block_sh;
 };
 hipError_t launch_rope_append(const RopeArgs& a, hipStream_t stream);
 
@@ -197,8 +201,14 @@ struct AttnArgs {
   const int32_t* lens;               // [B]
   int64_t B, Q, Hq, Hkv, D, max_blocks, window;
   float scale;
-  bool cache_e4m3;
-  const float *k_scale, *v_scale;    // E4M3 cache: float [1] each
+  float softcap;                     // > 0: scores z become softcap * tanh(z / softcap)
+  const float* slopes;               // float [Hq] or NULL: + slopes[head] * (key - token's position)
+  bool cache_e4m3, cache_nvfp4;
+  const float *k_scale, *v_scale;    // E4M3, NVFP4: float [1] each; bf16: NULL
+  // NVFP4: k_cache, v_cache hold the codes and sb, st, sh count bytes; the block
+  // scales, and their strides in bytes
+  const uint8_t *k_blocks, *v_blocks;
+  int64_t block_sb, block_st, block_sh;
   uint16_t* out;                     // bf16 [B * Q, Hq, D]
   void* workspace;
 };
@@ -206,6 +216,32 @@ struct AttnArgs {
 bool attn_fits(const AttnArgs& a);
 size_t attn_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv, int64_t D);
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream);
+// over an NVFP4 cache (paged_attn4.hip)
+int attn4_row_units(int64_t rows, int64_t Hkv, int64_t D);   // heads times row tiles
+size_t attn4_workspace_bytes(int64_t rows, int64_t Hkv, int64_t D);
+hipError_t launch_paged_attention4(const AttnArgs& a, hipStream_t stream);
+
+// Low-rank adapters on the outputs of projections of one input (lora.hip).
+struct LoraSegment {
+  const uint16_t *a, *b;             // bf16 [n_adapters, rank, K], [n_adapters, N, rank]
+  const float* base;                 // [M, N], NULL, or y
+  float* y;                          // [M, N]
+  int64_t N;
+  int blocks;                        // set by the launcher, as
+  bool wide;                         // 16-byte accesses of base and y
+};
+struct LoraArgs {
+  LoraSegment segs[kMaxSegments];
+  int n_segments;
+  const uint16_t* x;                 // bf16 [M, K]
+  const int32_t* ids;                // [M]
+  const int32_t* ranks;              // [n_adapters] or NULL
+  const float* alpha;                // [n_adapters] or NULL
+  int64_t n_adapters, rank, M, K;
+  void* workspace;
+};
+size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t rank, int64_t n_segments);
+hipError_t launch_lora(LoraArgs& a, hipStream_t stream);
 
 // Verification of drafted tokens (verify.hip).
 struct VerifyArgs {

@@ -19,6 +19,7 @@
 // fp32 30.6 us, 4.9 TB/s of reads and writes, a copy's rate (23.9 where the
 // arrays are found in the last cache).
 #include "elems.h"
+#include "divide.h"
 #include "internal.h"
 
 namespace nvfp4 {
@@ -34,6 +35,85 @@ struct RopeShape {
   int tpb;      // tokens per workgroup
   int parts;    // workgroups per token (tpb == 1 where parts > 1)
 };
+
+struct Nvfp4 {};   // a cache of E2M1 codes and E4M3 block scales
+
+// Block b (16 elements) of a head of k (turned where it lies in the first R) or
+// v to the NVFP4 cache, by one thread: the half layout's partners are read a
+// second time, from the cache, by their own block's thread. The encoders are
+// pack's and quantize_act's; a block that holds a NaN gets the scale NaN.
+template <typename TX, bool INTER>
+__device__ __forceinline__ void append_block(const TX* src, int b, bool turn, int half,
+                                             const float2* trig, float g, uint8_t* codes,
+                                             uint8_t* scale) {
+  Raw8<TX> raw[2], other[2];
+  const int e0 = b * 16;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = e0 + i * 8;
+    raw[i].load(src + e);
+    if (!INTER && turn) other[i].load(src + (e < half ? e + half : e - half));
+  }
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = e0 + i * 8;
+    float v[8];
+    raw[i].get(v);
+    if (turn && INTER) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float2 u = trig[e / 2 + p];
+        const float p0 = v[2 * p], p1 = v[2 * p + 1];
+        v[2 * p] = fmaf(p0, u.x, -(p1 * u.y));
+        v[2 * p + 1] = fmaf(p1, u.x, p0 * u.y);
+      }
+    } else if (turn) {
+      float w[8];
+      other[i].get(w);
+      const bool first = e < half;
+      const float2* tr = trig + (first ? e : e - half);
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        const float2 u = tr[p];
+        v[p] = fmaf(v[p], u.x, first ? -(w[p] * u.y) : w[p] * u.y);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < 8; ++p) x[i * 8 + p] = v[p];
+  }
+  uint32_t top = 0u;   // the largest magnitude's bits; a NaN's are above infinity's
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t u = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+    top = top > u ? top : u;
+  }
+  const float amax = __uint_as_float(top);
+  uint32_t lo = 0u, hi = 0u;
+  uint32_t sc = 0x7Fu;
+  if (top <= 0x7F800000u) {
+    sc = e4m3_encode(amax / (6.0f * g));
+    const float s = e4m3_to_f32<0>(sc);
+    if (s != 0.0f) {
+      const float d = s * g;
+      if (divides_fast(d, amax)) {
+        const float inv = 1.0f / d;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = quotient(x[i], d, inv);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = x[i] / d;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lo |= e2m1_encode(x[i]) << (4 * i);
+        hi |= e2m1_encode(x[8 + i]) << (4 * i);
+      }
+    }
+  }
+  *reinterpret_cast<u32x2_t*>(codes) = u32x2_t{lo, hi};
+  *scale = (uint8_t)sc;
+}
 
 template <typename TX, typename TC, bool INTER>
 __global__ __launch_bounds__(kThreads) void k_rope_append(const RopeArgs a, const RopeShape sh) {
@@ -51,8 +131,9 @@ __global__ __launch_bounds__(kThreads) void k_rope_append(const RopeArgs a, cons
     trig[i] = float2{c * a.rope_scale, s * a.rope_scale};
   }
   __syncthreads();
+  constexpr bool kFour = __is_same(TC, Nvfp4);
   float ks = 1.0f, vs = 1.0f;
-  if (sizeof(TC) == 1 && sh.Hkv) {
+  if ((kFour || sizeof(TC) == 1) && sh.Hkv) {
     ks = *a.k_scale;
     vs = *a.v_scale;
   }
@@ -68,6 +149,21 @@ __global__ __launch_bounds__(kThreads) void k_rope_append(const RopeArgs a, cons
     const TX* src = (const TX*)(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
                     t * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) +
                     (int64_t)head * sh.D;
+    if constexpr (kFour) {
+      if (kind != 0) {
+        const int64_t slot = a.slots[t];
+        const int64_t block = slot / a.page;
+        if (slot < 0 || block >= a.num_blocks) continue;
+        const int64_t place = slot - block * a.page;
+        append_block<TX, INTER>(
+            src, c, kind == 1 && c * 16 < sh.R, half, trig + tk * half, kind == 1 ? ks : vs,
+            (uint8_t*)(kind == 1 ? a.k_cache : a.v_cache) + block * a.sb + place * a.st +
+                head * a.sh + c * 8,
+            (kind == 1 ? a.k_blocks : a.v_blocks) + block * a.block_sb + place * a.block_st +
+                head * a.block_sh + c);
+        continue;
+      }
+    }
     // the two groups of 8: the chunk's pairs, or 16 elements as they are
     const bool turn = kind != 2 && c * 16 < sh.R;
     const int e0 = turn && !INTER ? c * 8 : c * 16;
@@ -105,7 +201,7 @@ __global__ __launch_bounds__(kThreads) void k_rope_append(const RopeArgs a, cons
       uint16_t* o = a.q_out + (t * sh.Hq + head) * sh.D;
       store8(o + e0, x0);
       store8(o + e1, x1);
-    } else {
+    } else if constexpr (!kFour) {
       const int64_t slot = a.slots[t];
       const int64_t block = slot / a.page;
       if (slot >= 0 && block < a.num_blocks) {
@@ -157,6 +253,8 @@ hipError_t launch_c(const RopeArgs& a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_rope_append(const RopeArgs& a, hipStream_t stream) {
+  if (a.cache_nvfp4)
+    return a.x_f32 ? launch_c<float, Nvfp4>(a, stream) : launch_c<uint16_t, Nvfp4>(a, stream);
   if (a.x_f32)
     return a.cache_e4m3 ? launch_c<float, uint8_t>(a, stream)
                         : launch_c<float, uint16_t>(a, stream);

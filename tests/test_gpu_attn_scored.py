@@ -1,0 +1,114 @@
+"""Attention over bf16 and E4M3 caches with capped scores and biases by
+distance against a plain 64-bit form; without either it is paged_attention."""
+import pytest
+import torch
+
+import nvfp4_block_scaled_gemv_amd as nv
+from gpu_util import DEV, say
+from serving_ref import attention, slopes_of
+from test_gpu_paged_attn import BF16, E4M3, build, run as run_plain, scales
+
+pytestmark = pytest.mark.gpu
+
+
+def run(q, table, lens, kc, vc, ks, vs, ct, slopes=None, **kw):
+    a, b = scales(ct, ks, vs)
+    out = nv.paged_attention_scored(q.to(DEV), kc, vc, table.to(DEV), lens.to(DEV), k_scale=a,
+                                    v_scale=b, slopes=None if slopes is None else slopes.to(DEV),
+                                    **kw)
+    torch.cuda.synchronize()
+    return out.cpu().double()
+
+
+def check(got, q, k, v, table, lens, scale, window, ks, vs, softcap, slopes):
+    """The bound of plain attention over these caches, with scores off by 2^-21 of
+    their largest more: the scale's products, the cap (2^-22 of it) and the bias
+    (its product and its addition, 2^-24 each) and the factors of log2."""
+    top = [0.0]
+
+    def weigh(z, w, vh):
+        top[0] = max(top[0], float(z.abs().max()))
+    kd, vd = k.double() * ks, v.double() * vs
+    ref = attention(q, kd, vd, table, lens, scale, window, softcap, slopes, weigh)
+    a = attention(q, kd, vd.abs(), table, lens, scale, window, softcap, slopes)
+    D = q.shape[-1]
+    size = float(q.double().norm(dim=-1).max() * kd.norm(dim=-1).max()) * abs(scale)
+    dz = 2 * D * 2.0 ** -24 * size + 2.0 ** -21 * top[0]
+    tol = a * (2.0 ** -23 + 2 * dz + 2.0 ** -14) + ref.abs() * 2.0 ** -8 + 1e-30
+    err = (got - ref).abs()
+    bad = ~(err <= tol)
+    assert not bad.any(), (int(bad.sum()), float((err / tol).max()), torch.nonzero(bad)[0].tolist())
+    return float((err / tol).max())
+
+
+CASES = [
+    # lens, Q, Hq, Hkv, D, page, type, window, order, softcap, bias
+    ([1], 1, 4, 1, 64, 16, BF16, 0, "nhd", 30.0, False),
+    ([700], 1, 32, 8, 128, 16, BF16, 0, "nhd", 50.0, False),
+    ([700], 1, 32, 8, 128, 16, E4M3, 0, "hnd", 0.0, True),
+    ([129, 0, 1, 64, 128, 500, 31], 1, 8, 2, 64, 32, BF16, 0, "nhd", 1.0, True),
+    ([1000, 3, 777], 5, 32, 8, 128, 64, BF16, 0, "nhd", 0.0, True),
+    ([1000, 3, 777], 5, 32, 8, 128, 64, E4M3, 300, "wide", 20.0, True),
+    ([300, 2], 3, 16, 16, 64, 20, BF16, 100, "nhd", 5.0, False),
+    ([260, 515], 2, 4, 4, 256, 16, BF16, 0, "nhd", 8.0, True),
+    ([260, 515], 2, 4, 4, 256, 1, E4M3, 0, "nhd", 0.0, True),
+    ([97, 200], 8, 8, 1, 128, 7, BF16, 0, "nhd", 0.01, False),
+    ([150, 1300], 5, 16, 2, 256, 16, E4M3, 90, "hnd", 12.0, False),
+    ([5000], 1, 8, 2, 128, 256, BF16, 0, "beside", 0.0, True),
+    ([2049], 64, 1, 1, 64, 128, BF16, 500, "nhd", 3.0, True),
+]
+
+
+@pytest.mark.parametrize("lens,Q,Hq,Hkv,D,page,ct,window,order,cap,bias", CASES)
+def test_scored(lens, Q, Hq, Hkv, D, page, ct, window, order, cap, bias):
+    say(f"[scored] lens={lens[:8]} x{len(lens)} Q={Q} Hq={Hq} Hkv={Hkv} D={D} page={page} {ct} "
+        f"window={window} {order} cap={cap} bias={bias}")
+    q, k, v, table, ln, kc, vc, ks, vs = build(lens, Q, Hq, Hkv, D, page, ct, order, seed=D + page)
+    q = q * 4
+    slopes = slopes_of(Hq) if bias else None
+    got = run(q, table, ln, kc, vc, ks, vs, ct, slopes, softcap=cap, window=window)
+    r = check(got, q, k, v, table, ln, D ** -0.5, window, ks, vs, cap, slopes)
+    say(f"  max err / tol = {r:.3f}")
+
+
+@pytest.mark.parametrize("ct", [BF16, E4M3])
+def test_without_either_it_is_paged_attention(ct):
+    args = build([1000, 33, 0], 2, 8, 2, 128, 16, ct, seed=2)
+    q, k, v, table, ln, kc, vc, ks, vs = args
+    want = run_plain(q, table, ln, kc, vc, ks, vs, ct, window=200)
+    assert torch.equal(run(q, table, ln, kc, vc, ks, vs, ct, window=200), want)
+    # slopes of zero: the same up to the bits that the addition of zero keeps
+    got = run(q, table, ln, kc, vc, ks, vs, ct, torch.zeros(8), window=200)
+    assert torch.equal(got, want)
+
+
+def test_slopes_of_either_sign_over_far_keys():
+    """Keys that are weighed more the farther they are, and less, 20000 of them."""
+    q, k, v, table, ln, kc, vc, ks, vs = build([20000], 1, 4, 2, 64, 64, BF16, seed=12)
+    slopes = torch.tensor([-2.0 ** -8, 2.0 ** -8, -1.0, 1.0])
+    got = run(q, table, ln, kc, vc, ks, vs, BF16, slopes)
+    check(got, q, k, v, table, ln, 0.125, 0, ks, vs, 0.0, slopes)
+
+
+@pytest.mark.parametrize("cap", [1e-6, 0.5, 1e30])
+def test_caps_at_the_ends(cap):
+    """A cap below every score leaves a plain mean, one above all changes nothing
+    that shows."""
+    q, k, v, table, ln, kc, vc, ks, vs = build([400], 2, 8, 2, 128, 16, BF16, seed=13)
+    got = run(q, table, ln, kc, vc, ks, vs, BF16, softcap=cap)
+    check(got, q, k, v, table, ln, 128 ** -0.5, 0, ks, vs, cap, None)
+
+
+def test_a_cap_makes_infinite_scores_finite():
+    """An infinite key's score is +-cap, a NaN one's NaN."""
+    q, k, v, table, ln, kc, vc, ks, vs = build([40], 1, 2, 1, 64, 16, BF16, seed=14)
+    q = torch.ones_like(q)
+    k[table[0, 0], 3, 0, 0] = float("inf")
+    kc.copy_(k)
+    got = run(q, table, ln, kc, vc, ks, vs, BF16, softcap=10.0)
+    k2 = k.clone()
+    k2[table[0, 0], 3, 0] = 1e30
+    check(got, q, k2.clamp(max=1e3), v, table, ln, 0.125, 0, ks, vs, 10.0, None)
+    k[table[0, 0], 3, 0, 0] = float("nan")
+    kc.copy_(k)
+    assert torch.isnan(run(q, table, ln, kc, vc, ks, vs, BF16, softcap=10.0)).all()
