@@ -5,6 +5,8 @@
 // are classes derived from AttnPass.
 #pragma once
 
+#include <type_traits>
+
 #include "elems.h"
 #include "attn_span.h"
 #include "internal.h"
@@ -25,7 +27,8 @@ constexpr int kMaxRuns = kCus * 4 * 2;
 struct AttnShape {
   int rows;        // G * Q
   int G;
-  int NHV;         // heads as the wavefronts see them: Hkv * row tiles
+  int heads;       // key-value heads that a wavefront takes side by side
+  int NHV;         // heads as the wavefronts see them: Hkv / heads * row tiles
   int groups;      // runs
   int page_shift;  // log2(page), or -1
   int cap;         // keys that a row of the table can name
@@ -36,8 +39,9 @@ struct AttnShape {
 
 typedef const __attribute__((address_space(4))) int32_t* const_i32;
 
+template <int TILE>
 __device__ __forceinline__ Span span_of(const AttnArgs& a, const AttnShape& sh, int len) {
-  return nvfp4::span_of(len, sh.cap, a.Q, a.window);
+  return nvfp4::span_of<TILE>(len, sh.cap, a.Q, a.window);
 }
 
 // Inclusive sums over the 64 lanes, by DPP: within rows of 16, then from each
@@ -53,6 +57,7 @@ __device__ __forceinline__ int scan64(int v) {
 }
 
 // The tiles of all sequences, by every wavefront for itself (all 64 lanes).
+template <int TILE>   // keys per tile
 struct Tiles {
   const AttnArgs& a;
   const AttnShape& sh;
@@ -62,12 +67,12 @@ struct Tiles {
   __device__ __forceinline__ Tiles(const AttnArgs& a_, const AttnShape& sh_)
       : a(a_), sh(sh_), lane(threadIdx.x & 63) {
     len = lane < (int)a.B ? a.lens[lane] : 0;
-    n = lane < (int)a.B ? span_of(a, sh, len).n : 0;
+    n = lane < (int)a.B ? span_of<TILE>(a, sh, len).n : 0;
     incl = scan64(n);
     total = __builtin_amdgcn_readlane(incl, 63);
     for (int b0 = 64; b0 < (int)a.B; b0 += 64) {
       const int b = b0 + lane;
-      const int m = b < (int)a.B ? span_of(a, sh, a.lens[b]).n : 0;
+      const int m = b < (int)a.B ? span_of<TILE>(a, sh, a.lens[b]).n : 0;
       total += __builtin_amdgcn_readlane(scan64(m), 63);
     }
   }
@@ -86,7 +91,7 @@ struct Tiles {
       b0 += 64;
       if (b0 >= (int)a.B) break;   // not reached for u below the total
       len_l = b0 + lane < (int)a.B ? a.lens[b0 + lane] : 0;
-      n_l = b0 + lane < (int)a.B ? span_of(a, sh, len_l).n : 0;
+      n_l = b0 + lane < (int)a.B ? span_of<TILE>(a, sh, len_l).n : 0;
       incl_l = scan64(n_l);
     }
     before = its_len = 0;
@@ -98,7 +103,7 @@ struct Tiles {
     for (int b0 = 0; b - b0 >= 64;) {
       run += __builtin_amdgcn_readlane(incl_l, 63);
       b0 += 64;
-      n_l = b0 + lane < (int)a.B ? span_of(a, sh, a.lens[b0 + lane]).n : 0;
+      n_l = b0 + lane < (int)a.B ? span_of<TILE>(a, sh, a.lens[b0 + lane]).n : 0;
       incl_l = scan64(n_l);
     }
     return run + __builtin_amdgcn_readlane(incl_l - n_l, b & 63);
@@ -139,6 +144,14 @@ __device__ __forceinline__ float tanh_32(float x) {
   return copysignf(y < 0.3f ? p : big, x);
 }
 
+// LDS is written and read by the lanes of one wavefront, in order: the compiler
+// has to keep that order across lanes too.
+__device__ __forceinline__ void in_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // A tile of a wavefront's run.
 struct Cursor {
   int b, len;   // its sequence
@@ -147,33 +160,42 @@ struct Cursor {
 };
 
 // A wavefront's pass over tiles of one head, for a class W derived from it that
-// holds K and V of a tile and the sums O. NU = TK / 16 runs of 16 keys make a
-// tile; RT tiles of 16 rows share it. Score e (of TK / 4) of a lane is row rt *
-// 16 + n and key W::key_of(e, g) of the tile. PG: pages hold whole runs of 16
-// keys. MOD: the scores are capped or biased.
-template <class W, int RT, bool PG, bool MOD>
+// holds K and V of a tile of TILE keys and the sums O; RT tiles of 16 rows share
+// it. Score e (of TILE / 4) of a lane is row rt * 16 + n and key W::key_of(e, g)
+// of the tile. RUN: pages hold whole runs of that many keys (0: they do not).
+// HEADS: key-value heads from h on that the wavefront takes side by side (2, where
+// their rows fit): the 16 columns of a tile of rows are then HEADS blocks.
+// MOD: the scores are capped or biased. W::kStage: bytes of LDS that a wavefront
+// takes V through (0: none), in W::take_v().
+template <class W, int TILE, int RT, int RUN, bool MOD, int HEADS = 1>
 struct AttnPass {
+  static_assert(HEADS == 1 || RT == 1, "heads side by side: one tile of rows");
+  static constexpr int kTile = TILE;
+  static constexpr int kHeads = HEADS;
+  static constexpr int kCols = 16 / HEADS;     // columns per head
   static constexpr int kRT = RT;
-  static constexpr int NU = TK / 16;           // runs of 16 keys
-  static constexpr int NO = PG ? NU : 1;
-  static constexpr uint32_t kAll = 0xFFFFFFFFu;
+  static constexpr int NU = TILE / 16;         // runs of 16 keys
+  static constexpr int NO = RUN ? TILE / RUN : 1;
+  typedef typename std::conditional<TILE == 64, uint64_t, uint32_t>::type Mask;   // bit per key
+  static constexpr Mask kAll = ~(Mask)0;
 
   const AttnArgs& a;
   const AttnShape& sh;
   const const_i32 lens;
   const int lane, n, g;
   const int h, Q, G, row0, rows;
+  const int hl, col;                           // the lane's head from h on, and its row there
   int len_after;                               // of the sequence after the last cursor's
   int tok[RT];
   const float c;                               // scale of the scores, log2 (cap: of tanh's argument)
   float slope[RT];                             // of the row's head, log2 (MOD)
   float m[RT], l[RT];
   // Where a tile's keys lie. fetch() reads the page numbers, a tile ahead of
-  // resolve(), which turns them into places: PG, runs of 16 keys inside one
-  // page each (uniform); otherwise one place per lane, for key lane % TK. ok:
-  // bit per key, its page exists (page 0 is read in its place).
+  // resolve(), which turns them into places: of runs of keys inside one page
+  // each (uniform), or one per lane, for key lane % TILE. ok: bit per key, its
+  // page exists (page 0 is read in its place).
   int ids[NO], in_page[NO];
-  uint32_t ok;
+  Mask ok;
 
   __device__ __forceinline__ W& self() { return *static_cast<W*>(this); }
   __device__ __forceinline__ AttnPass(const AttnArgs& a_, const AttnShape& sh_, int h_, int row0_,
@@ -181,25 +203,28 @@ struct AttnPass {
       : a(a_), sh(sh_), lens((const_i32)(uintptr_t)a_.lens), lane(threadIdx.x & 63),
         n(lane & 15), g(lane >> 4), h(h_), Q((int)a_.Q), G(sh_.G), row0(row0_),
         rows(sh_.rows - row0_ < RT * 16 ? sh_.rows - row0_ : RT * 16),
+        hl(HEADS == 1 ? 0 : n / kCols), col(HEADS == 1 ? n : n % kCols),
         c(MOD && a_.softcap > 0.0f ? a_.scale * k_scale / a_.softcap
                                    : a_.scale * k_scale * kLog2e) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int r = row0 + rt * 16 + n;
+      const int r = row0 + rt * 16 + col;
       tok[rt] = r < sh.rows ? r / G : -1;
-      if (MOD) slope[rt] = a.slopes && tok[rt] >= 0 ? a.slopes[h * G + r - tok[rt] * G] * kLog2e : 0.0f;
+      if (MOD)
+        slope[rt] = a.slopes && tok[rt] >= 0
+                        ? a.slopes[(h + hl) * G + r - tok[rt] * G] * kLog2e : 0.0f;
     }
   }
   __device__ __forceinline__ Cursor first_of(int b, int len, int idx) {
-    const Span s = span_of(a, sh, len);
+    const Span s = span_of<TILE>(a, sh, len);
     len_after = lens[b + 1 < (int)a.B ? b + 1 : b];
-    return Cursor{b, s.len, s.base + idx * TK, s.n - idx};
+    return Cursor{b, s.len, s.base + idx * TILE, s.n - idx};
   }
   // The tile `step` further in c's sequence, or the next one's first (past the
   // last sequence: any tile, it is not computed).
   __device__ __forceinline__ Cursor after(const Cursor& c, int step) {
     if (c.left <= step && c.b + 1 < (int)a.B) return first_of(c.b + 1, len_after, 0);
-    return Cursor{c.b, c.len, tile_after(c.key, step), c.left - step};
+    return Cursor{c.b, c.len, tile_after<TILE>(c.key, step), c.left - step};
   }
 
   __device__ __forceinline__ int page_of(int key, int ahead, int& in) const {
@@ -207,12 +232,12 @@ struct AttnPass {
   }
   // Only for tiles that hold a key: an empty sequence's table has no row.
   __device__ __forceinline__ void fetch(const Cursor& c) {
-    if constexpr (PG) {
+    if constexpr (RUN != 0) {
       const const_i32 table = (const_i32)(uintptr_t)(a.table + (int64_t)c.b * a.max_blocks);
 #pragma unroll
-      for (int u = 0; u < NU; ++u) ids[u] = table[page_of(c.key, 16 * u, in_page[u])];
+      for (int u = 0; u < NO; ++u) ids[u] = table[page_of(c.key, RUN * u, in_page[u])];
     } else {
-      const int pi = page_of(c.key, lane & (TK - 1), in_page[0]);
+      const int pi = page_of(c.key, lane & (TILE - 1), in_page[0]);
       ids[0] = a.table[(int64_t)c.b * a.max_blocks + pi];
     }
   }
@@ -222,10 +247,10 @@ struct AttnPass {
     for (int u = 0; u < NO; ++u) {
       const bool fine = (uint32_t)ids[u] < (uint32_t)a.num_blocks;
       self().place(u, fine ? ids[u] : 0, in_page[u]);
-      if (PG)
-        ok |= fine ? 0xFFFFu << (16 * u) : 0u;
+      if (RUN != 0)
+        ok |= fine ? (kAll >> (TILE - (RUN ? RUN : TILE))) << (RUN * u) : (Mask)0;
       else
-        ok = (uint32_t)__ballot(fine);
+        ok = (Mask)__ballot(fine);
     }
   }
   // lane src's 64 bits
@@ -279,7 +304,7 @@ struct AttnPass {
       f32x4_t S[RT][NU];
       typename W::Weights pf;
       w.scores(S);
-      const uint32_t ok_now = ok;
+      const Mask ok_now = ok;
       resolve();
       w.load_k(more);
       const Cursor nxt2 = after(nxt, step);
@@ -287,7 +312,7 @@ struct AttnPass {
       if (MOD) modify(S, cur);
       // every row sees the whole tile
       const int pos0 = cur.len - Q;
-      const bool all = ok_now == kAll && cur.key + TK - 1 <= pos0 &&
+      const bool all = ok_now == kAll && cur.key + TILE - 1 <= pos0 &&
                        (!a.window || cur.key >= (int64_t)cur.len - a.window);
       uint32_t weightless[RT];
       if (!all) {
@@ -307,19 +332,21 @@ struct AttnPass {
         }
       }
       w.softmax(S, pf);
+      w.take_v();
+      if (W::kStage) w.load_v(more);   // V is in LDS: its registers are free
       if (!all) {
         // Values that no row sees may be anything: they become zero.
         const int last = cur.len - Q + t1;
         const int64_t firsts = a.window ? (int64_t)cur.len - Q + t0 - a.window + 1 : 0;
 #pragma unroll
-        for (int e = 0; e < TK / 4; ++e) {
+        for (int e = 0; e < TILE / 4; ++e) {
           const int key = cur.key + W::key_of(e, g);
           w.keep(e, key <= last && key >= firsts && ((ok_now >> W::key_of(e, g)) & 1u));
         }
-        if (t1 > t0) settle(weightless);
+        if (t1 > t0) w.settle(weightless);
       }
       w.values(pf);
-      w.load_v(more);
+      if (!W::kStage) w.load_v(more);
       if (!more || nxt.b != cur.b) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {   // a row's four lanes (their maxima are the same)
@@ -338,25 +365,17 @@ struct AttnPass {
       nxt = nxt2;
     }
   }
-  // A key that some rows see and others do not has weight 0 for these, which is
-  // enough unless its value is infinite or NaN (0 * inf would reach them). Such
-  // a value becomes zero, and the sum of the rows that see it NaN. weightless:
-  // bit e, this lane's row does not see key e.
-  __device__ __forceinline__ void settle(const uint32_t (&weightless)[RT]) {
-#pragma unroll
-    for (int e = 0; e < TK / 4; ++e) {
-      const bool bad = self().not_finite(e);
-      self().keep(e, !bad);
-      const bool any = (__ballot(bad) >> (16 * g)) & 0xFFFFu;   // of the key's 16 lanes
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-        if (any && !((weightless[rt] >> e) & 1u)) l[rt] = __builtin_nanf("");
-    }
-  }
 };
 
 __device__ __forceinline__ void store4(uint16_t* p, f32x4_t v) {
   *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+}
+
+// Workgroups go to the 8 XCDs in turn; of n the b-th becomes one of n / 8
+// neighbours on its XCD.
+__device__ __forceinline__ int on_one_xcd(int b, int n) {
+  const int x = b & 7, q = n >> 3, r = n & 7;
+  return x * q + (x < r ? x : r) + (b >> 3);
 }
 
 // The split form: a wavefront per (run, head).
@@ -364,17 +383,20 @@ template <class Wave>
 __global__ __launch_bounds__(256, Wave::kPerSimd) void k_attn_runs(const AttnArgs a,
                                                                    const AttnShape sh) {
   constexpr int D = Wave::kD, RT = Wave::kRT;
-  const Tiles tiles(a, sh);
+  __shared__ __align__(16) uint8_t stage[4][Wave::kStage ? Wave::kStage : 16];
+  const Tiles<Wave::kTile> tiles(a, sh);
   const Runs runs(tiles.total, sh.groups);
-  const int unit = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int block = Wave::kStage ? on_one_xcd(blockIdx.x, gridDim.x) : (int)blockIdx.x;
+  const int unit = block * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int w = unit / sh.NHV, hv = unit - w * sh.NHV;
   if (w >= runs.nw) return;
-  const int rt_tile = hv / (int)a.Hkv, h = hv - rt_tile * (int)a.Hkv;
+  const int all_heads = (int)a.Hkv / Wave::kHeads;
+  const int rt_tile = hv / all_heads, h = (hv - rt_tile * all_heads) * Wave::kHeads;
   const int s = runs.start(w), count = runs.start(w + 1) - s;
   int before, len;
   const int b = tiles.find(s, before, len);
   const float ks = Wave::kScaled ? *a.k_scale : 1.0f, vs = Wave::kScaled ? *a.v_scale : 1.0f;
-  Wave wave(a, sh, h, rt_tile * (RT * 16), ks);
+  Wave wave(a, sh, h, rt_tile * (RT * 16), ks, stage[threadIdx.x >> 6]);
   bool from_start = s == before;
   int64_t rec = (int64_t)(w * sh.NHV + hv) * 2 * sh.slot_rows;
   wave.pass(wave.first_of(b, len, s - before), count, 1, [&](const Cursor& c) {
@@ -382,11 +404,12 @@ __global__ __launch_bounds__(256, Wave::kPerSimd) void k_attn_runs(const AttnArg
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       if (wave.tok[rt] < 0) continue;
-      const int r = rt * 16 + wave.n;
+      const int row = rt * 16 + wave.col, r = Wave::kHeads == 1 ? row : wave.hl * sh.rows + row;
       if (whole) {
         const float f = wave.l[rt] == 0.0f ? 0.0f : vs / wave.l[rt];
-        uint16_t* o = a.out + ((int64_t)(c.b * a.Q + wave.tok[rt]) * a.Hq + h * sh.G +
-                               (wave.row0 + r - wave.tok[rt] * sh.G)) * D;
+        uint16_t* o = a.out + ((int64_t)(c.b * a.Q + wave.tok[rt]) * a.Hq +
+                               (h + wave.hl) * sh.G +
+                               (wave.row0 + row - wave.tok[rt] * sh.G)) * D;
         wave.each4(rt, [&](int d, f32x4_t v) { store4(o + d, v * f); });
       } else {
         if (wave.g == 0) {
@@ -409,16 +432,19 @@ template <class Wave>
 __global__ __launch_bounds__(kWholeWaves * 64, 2) void k_attn_whole(const AttnArgs a,
                                                                     const AttnShape sh) {
   constexpr int D = Wave::kD, RT = Wave::kRT;
-  __shared__ float lds_o[kWholeWaves][RT * 16][D + 4];
+  // a wavefront's sums, and before them the LDS of its pass
+  __shared__ __align__(16) float lds_o[kWholeWaves][RT * 16][D + 4];
+  static_assert(Wave::kStage <= (int)sizeof(lds_o[0]), "the pass's LDS");
   __shared__ float lds_ml[kWholeWaves][RT * 16][2];
   const int b = blockIdx.x / sh.NHV, hv = blockIdx.x - b * sh.NHV;
   const int rt_tile = hv / (int)a.Hkv, h = hv - rt_tile * (int)a.Hkv;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const float ks = Wave::kScaled ? *a.k_scale : 1.0f, vs = Wave::kScaled ? *a.v_scale : 1.0f;
   const int len = ((const_i32)(uintptr_t)a.lens)[b];
-  Wave wave(a, sh, h, rt_tile * (RT * 16), ks);
-  const int count = (span_of(a, sh, len).n - wv + kWholeWaves - 1) / kWholeWaves;
+  Wave wave(a, sh, h, rt_tile * (RT * 16), ks, (uint8_t*)lds_o[wv]);
+  const int count = (span_of<Wave::kTile>(a, sh, len).n - wv + kWholeWaves - 1) / kWholeWaves;
   if (count > 0) wave.pass(wave.first_of(b, len, wv), count, kWholeWaves, [](const Cursor&) {});
+  if (Wave::kStage) in_order();
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
     if (wave.g == 0) {
@@ -456,19 +482,21 @@ __global__ __launch_bounds__(kWholeWaves * 64, 2) void k_attn_whole(const AttnAr
 // One workgroup per (sequence, head, row) of a sequence that several runs
 // share: the records' weights first, then groups of D / 4 threads add the
 // records in turn and meet in LDS.
-template <int D>
+template <int D, int TILE>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnShape sh) {
   constexpr int TD = D / 4, NG = 256 / TD;
   __shared__ float lds[NG][D + 4];
   __shared__ float lds_f[kMaxRuns];
   __shared__ float lds_red[2][4];
   const int b = blockIdx.x / sh.NHV, hv = blockIdx.x % sh.NHV, r = blockIdx.y;
-  const int rt_tile = hv / (int)a.Hkv, h = hv - rt_tile * (int)a.Hkv;
-  const int rr = rt_tile * sh.slot_rows + r;
+  const int all_heads = (int)a.Hkv / sh.heads;
+  const int rt_tile = hv / all_heads, hl = sh.heads == 1 ? 0 : r / sh.rows;
+  const int h = (hv - rt_tile * all_heads) * sh.heads + hl;
+  const int rr = rt_tile * sh.slot_rows + r - hl * sh.rows;
   if (rr >= sh.rows) return;
-  const Tiles tiles(a, sh);
+  const Tiles<TILE> tiles(a, sh);
   const Runs runs(tiles.total, sh.groups);
-  const int s0 = tiles.before(b), nb = span_of(a, sh, a.lens[b]).n;
+  const int s0 = tiles.before(b), nb = span_of<TILE>(a, sh, a.lens[b]).n;
   const int lane = threadIdx.x & 63;
   const int w0 = runs.of(s0), w1 = runs.of(s0 + nb - 1);
   if (w0 == w1) return;   // finished by its one wavefront
@@ -541,13 +569,14 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnS
 // wavefronts), and where their records lie in the workspace.
 struct AttnLayout {
   size_t ml, o, total;
-  int RT, slot_rows, NHV, groups;
+  int RT, heads, slot_rows, NHV, groups;
 };
-AttnLayout attn_layout(int64_t rows, int64_t Hkv, int64_t D, int RT, int per_simd) {
+AttnLayout attn_layout(int64_t rows, int64_t Hkv, int64_t D, int RT, int per_simd, int heads = 1) {
   AttnLayout L;
   L.RT = RT;
-  L.NHV = (int)(Hkv * ((rows + L.RT * 16 - 1) / (L.RT * 16)));
-  L.slot_rows = (int)(rows < L.RT * 16 ? rows : L.RT * 16);
+  L.heads = heads;
+  L.NHV = (int)(Hkv / heads * ((rows + L.RT * 16 - 1) / (L.RT * 16)));
+  L.slot_rows = (int)(heads * (rows < L.RT * 16 ? rows : L.RT * 16));
   L.groups = kCus * 4 * per_simd / L.NHV;
   if (L.groups < 1) L.groups = 1;
   const size_t slots = (size_t)2 * L.groups * L.NHV;
@@ -573,6 +602,7 @@ AttnShape attn_shape(const AttnArgs& a, const AttnLayout& L) {
   AttnShape sh;
   sh.G = (int)(a.Hq / a.Hkv);
   sh.rows = sh.G * (int)a.Q;
+  sh.heads = L.heads;
   sh.NHV = L.NHV;
   sh.groups = L.groups;
   sh.cap = capacity(a);
@@ -595,21 +625,21 @@ hipError_t launch_forms(const AttnArgs& a, AttnShape sh, int64_t whole, hipStrea
   // Heads of 256 have no whole form: eight wavefronts leave 256 registers each,
   // which two row tiles of 128 fill already (4 to 53 VGPRs spill in three of the
   // four bf16 and E4M3 forms).
-  if constexpr (D < 256) {
+  if constexpr (D < 256 && Wave::kHeads == 1) {
     if (keys <= whole) {
       hipLaunchKernelGGL((k_attn_whole<Wave>), dim3((uint32_t)(a.B * sh.NHV)),
                          dim3(kWholeWaves * 64), 0, stream, a, sh);
       return hipGetLastError();
     }
   }
-  const int64_t most = (keys + TK - 1) / TK * a.B;   // tiles
+  const int64_t most = (keys + Wave::kTile - 1) / Wave::kTile * a.B;   // tiles
   if (most < sh.groups) sh.groups = (int)most;
   const int64_t units = (int64_t)sh.groups * sh.NHV;
   hipLaunchKernelGGL((k_attn_runs<Wave>), dim3((uint32_t)((units + 3) / 4)), dim3(256), 0, stream,
                      a, sh);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || keys <= TK) return e;   // a sequence of one tile is never shared
-  hipLaunchKernelGGL((k_attn_join<D>),
+  if (e != hipSuccess || keys <= Wave::kTile) return e;   // a sequence of one tile is never shared
+  hipLaunchKernelGGL((k_attn_join<D, Wave::kTile>),
                      dim3((uint32_t)(a.B * sh.NHV), (uint32_t)sh.slot_rows), dim3(256), 0, stream,
                      a, sh);
   return hipGetLastError();

@@ -103,13 +103,14 @@ struct VRow {
 
 // K, V and O of one wavefront's pass over tiles of one head.
 template <int D, bool FP8, int RT, bool PG, bool MOD>
-struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD>, RT, PG, MOD> {
-  using Pass = AttnPass<AttnWave, RT, PG, MOD>;
+struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD>, TK, RT, PG ? 16 : 0, MOD> {
+  using Pass = AttnPass<AttnWave, TK, RT, PG ? 16 : 0, MOD>;
   using Pass::a, Pass::sh, Pass::n, Pass::g, Pass::h, Pass::Q, Pass::G, Pass::row0, Pass::c,
       Pass::tok, Pass::m, Pass::l, Pass::NU, Pass::NO;
   static constexpr int kD = D;
   static constexpr bool kScaled = FP8;
   static constexpr int kPerSimd = waves_per_simd(RT, D, FP8);
+  static constexpr int kStage = 0;
   static constexpr int NP = TK / 32;           // products over the keys
   static constexpr int NJ = D / 32;            // products over the dims
   static constexpr int NV = D / 16;            // dims per lane of V
@@ -127,7 +128,7 @@ struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD>, RT, PG, MOD> {
   int64_t off[NO];                             // elements, from place()
 
   __device__ __forceinline__ AttnWave(const AttnArgs& a_, const AttnShape& sh_, int h_, int row0_,
-                                      float k_scale)
+                                      float k_scale, uint8_t*)
       : Pass(a_, sh_, h_, row0_, k_scale), head_off((int64_t)h_ * a_.sh),
         stb((uint32_t)a_.st * ES), k_lane((uint32_t)n * stb + (uint32_t)g * 16),
         v_dim((uint32_t)n * (NV > 8 ? 8 : NV) * ES), v_lane((uint32_t)(g * 4) * stb + v_dim) {
@@ -194,6 +195,8 @@ struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD>, RT, PG, MOD> {
       vr[i].load(PG ? vc + off[PG ? i >> 2 : 0] * ES + (uint32_t)(i & 3) * st + lane_off
                     : want ? vc + at_key(key_of(i, g)) + v_dim : vc);
   }
+
+  __device__ __forceinline__ void take_v() {}
 
   // S^T of the loaded tile, scaled
   __device__ __forceinline__ void scores(f32x4_t (&S)[RT][NU]) {
@@ -292,7 +295,21 @@ struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD>, RT, PG, MOD> {
 #pragma unroll
     for (int d = 0; d < VRow<NV, FP8>::kDw; ++d) vr[e].w[d] = see ? vr[e].w[d] : 0u;
   }
-  __device__ __forceinline__ bool not_finite(int e) const { return vr[e].not_finite(); }
+  // A key that some rows see and others do not has weight 0 for these, which is
+  // enough unless its value is infinite or NaN (0 * inf would reach them). Such
+  // a value becomes zero, and the sum of the rows that see it NaN. weightless:
+  // bit e, this lane's row does not see key e.
+  __device__ __forceinline__ void settle(const uint32_t (&weightless)[RT]) {
+#pragma unroll
+    for (int e = 0; e < TK / 4; ++e) {
+      const bool bad = vr[e].not_finite();
+      keep(e, !bad);
+      const bool any = (__ballot(bad) >> (16 * g)) & 0xFFFFu;   // of the key's 16 lanes
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        if (any && !((weightless[rt] >> e) & 1u)) l[rt] = __builtin_nanf("");
+    }
+  }
 
   // O^T row g * 4 + i of the products is dims (g * 4 + i) * 8 .. + 7 (heads of
   // 64: * 4 .. + 3; of 256: products 8 .. 15 are the second half). f(d0, v): 4
