@@ -187,3 +187,18 @@ def test_adapters_past_4_gib():
     a[at], b[at] = mats[0][0].to(DEV), mats[0][1].to(DEV)
     got = nv.lora_segments([(a, b)], x.to(DEV), at.to(torch.int32))[0].cpu().double()
     check([got], mats, x, torch.arange(3, dtype=torch.int32))
+
+
+def test_one_launch_and_two_give_the_same_bits():
+    """Few rows of a small rank take one launch, many two; the order of every sum
+    is the same: a row alone gives the bits that it has among 128."""
+    for K, rank, Ns in ((4096, 16, [300, 8]), (1056, 8, [1025]), (5152, 8, [64])):
+        g, mats, x = make(128, K, Ns * 2, 8, rank, seed=K)
+        mats = mats[:len(Ns)]
+        ids = torch.randint(0, 8, (128,), generator=g, dtype=torch.int32)
+        wide = [(a, b.repeat(1, 12, 1)) for a, b in mats]    # more outputs: two launches
+        many = run(wide, x, ids)
+        for m in (0, 77, 127):
+            alone = run(mats, x[m:m + 1], ids[m:m + 1])
+            for y, z, n in zip(alone, many, Ns):
+                assert torch.equal(y[0], z[m, :n])
