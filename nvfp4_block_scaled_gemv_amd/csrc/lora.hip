@@ -387,15 +387,16 @@ bool all_in_one(const LoraArgs& a, const LoraShape& sh) {
   return a.rank * a.K <= 1 << 16 && a.M * blocks <= 192;
 }
 
-// Outputs of a workgroup of k_lora_up: more where there are many, for fewer starts
-// (ids, sums, first loads). One block of 256 against up to four, us, both kernels:
-// 128 rows of as many adapters, 6144 outputs, rank 16 27.1 / 24.7; 64, rank 64 40.9 /
-// 40.7; 128 rows of one adapter 16.2 / 18.8.
+// Outputs of a workgroup of k_lora_up: two blocks of 256 where there are many, for
+// fewer starts (ids, sums, first loads). One, two or four blocks, both kernels, us:
+// 128 rows of as many adapters, 6144 outputs, rank 16 27.1 / 25.5 / 24.3; 48 rows of 38
+// adapters of ranks 16 to 64, 24576 outputs 42.7 / 42.4 / 44.0; 128 rows of one adapter
+// 16.2 / 17.6 / 18.8.
 int outs_of(const LoraArgs& a) {
   int64_t blocks = 0;
   for (int s = 0; s < a.n_segments; ++s) blocks += (a.segs[s].N + kOuts - 1) / kOuts;
   const int64_t each = a.M * blocks / 1024;
-  return kOuts * (int)(each < 1 ? 1 : each > 4 ? 4 : each);
+  return kOuts * (int)(each < 1 ? 1 : each > 2 ? 2 : each);
 }
 
 }  // namespace

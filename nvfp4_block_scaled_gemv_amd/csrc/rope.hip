@@ -38,6 +38,23 @@ struct RopeShape {
 
 struct Nvfp4 {};   // a cache of E2M1 codes and E4M3 block scales
 
+// Eight E2M1 codes, nibble i of x[i], as e2m1_encode gives them (compared on the
+// card for every fp32 but NaN): the conversion rounds to the nearest even code, the
+// rest is its saturation and the sign of zero. A chain of comparisons for each
+// instead: 4099 tokens of 8 heads of 128 28.1 -> 21.2 us.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&x)[16], int at) {
+  float c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = fminf(fmaxf(x[at + i], -6.0f), 6.0f);
+  uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, c[0], c[1], 1.0f, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, c[2], c[3], 1.0f, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, c[4], c[5], 1.0f, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, c[6], c[7], 1.0f, 3);
+  const uint32_t mag = w & 0x77777777u;
+  const uint32_t some = (mag | (mag >> 1) | (mag >> 2)) & 0x11111111u;   // not zero
+  return mag | (w & (some << 3));
+}
+
 // Block b (16 elements) of a head of k (turned where it lies in the first R) or
 // v to the NVFP4 cache, by one thread: the half layout's partners are read a
 // second time, from the cache, by their own block's thread. The encoders are
@@ -104,11 +121,8 @@ __device__ __forceinline__ void append_block(const TX* src, int b, bool turn, in
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = x[i] / d;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        lo |= e2m1_encode(x[i]) << (4 * i);
-        hi |= e2m1_encode(x[8 + i]) << (4 * i);
-      }
+      lo = e2m1x8(x, 0);
+      hi = e2m1x8(x, 8);
     }
   }
   *reinterpret_cast<u32x2_t*>(codes) = u32x2_t{lo, hi};
