@@ -343,7 +343,15 @@ struct AttnPass {
           const int key = cur.key + W::key_of(e, g);
           w.keep(e, key <= last && key >= firsts && ((ok_now >> W::key_of(e, g)) & 1u));
         }
-        if (t1 > t0) w.settle(weightless);
+        if (HEADS == 1 && t1 > t0) w.settle(weightless);
+      }
+      // heads side by side: another head's values have weight 0 for a row, always
+      if constexpr (HEADS > 1) {
+        if (w.any_nan()) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) weightless[rt] = all ? 0u : weightless[rt];
+          w.settle(weightless);
+        }
       }
       w.values(pf);
       if (!W::kStage) w.load_v(more);

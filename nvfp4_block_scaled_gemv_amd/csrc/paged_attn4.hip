@@ -435,10 +435,17 @@ struct Attn4Wave
     constexpr uint32_t kKey = 0xFFFFFFFFu >> (32 - 8 * HEADS);
     vb[e / PU] &= see ? 0xFFFFFFFFu : ~(kKey << (e % PU * 8 * HEADS));
   }
-  // A key that some rows see and others do not has weight 0 for these, which is
-  // enough unless its value is NaN (its scale is: 0 times it would reach them).
-  // Such a value becomes zero, and the sum of the rows that see it NaN.
-  // weightless: bit e, this lane's row does not see key e.
+  // Some scale of V's tile is NaN: a byte whose lower 7 bits are set.
+  __device__ __forceinline__ bool any_nan() const {
+    uint32_t hit = 0u;
+#pragma unroll
+    for (int u = 0; u < NU; ++u) hit |= (vb[u] & 0x7F7F7F7Fu) + 0x01010101u;
+    return __any((hit & 0x80808080u) != 0u);
+  }
+  // A key that some rows see and others do not (and, of two heads, the other's
+  // rows never) has weight 0 for these, which is enough unless its value is NaN
+  // (0 times it would reach them). Such a value becomes zero, and the sum of the
+  // rows that see it NaN. weightless: bit e, this lane's row does not see key e.
   __device__ __forceinline__ void settle(const uint32_t (&weightless)[RT]) {
 #pragma unroll
     for (int s = 0; s < 16; ++s) {

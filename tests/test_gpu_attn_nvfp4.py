@@ -91,6 +91,57 @@ def test_attention(lens, Q, Hq, Hkv, D, page, window, order, cap, bias):
     say(f"  max err / tol = {r:.3f}")
 
 
+WIDE_CASES = [
+    # lens, Q, Hq, Hkv, D, page, window, order, softcap, bias: rows of a head that fit
+    # beside another's, tables of 2^18 keys of all heads and more
+    ([1], 1, 2, 2, 64, 16, 0, "nhd", 0.0, False),
+    ([700, 33, 0, 64], 1, 32, 8, 128, 16, 0, "nhd", 0.0, False),
+    ([700, 33, 0, 64], 1, 32, 8, 128, 64, 0, "hnd", 20.0, True),
+    ([129, 5000], 1, 16, 2, 128, 256, 0, "beside", 0.0, False),   # 8 rows
+    ([1000, 3, 777], 2, 16, 4, 128, 32, 0, "wide", 0.0, True),    # 8 rows, two tokens
+    ([300, 2, 95], 3, 4, 4, 64, 20, 100, "nhd", 0.0, False),
+    ([300, 2, 95], 8, 2, 2, 64, 7, 30, "hnd", 4.0, False),
+    ([260, 515], 2, 12, 4, 256, 16, 0, "nhd", 0.0, False),
+    ([260, 515], 1, 14, 2, 256, 20, 0, "wide", 0.0, True),
+    ([97, 200], 5, 6, 6, 256, 64, 48, "beside", 0.0, False),
+    ([63] * 70, 1, 4, 4, 64, 16, 0, "nhd", 0.0, False),
+    ([20000, 17], 1, 8, 2, 128, 16, 0, "nhd", 0.0, False),
+    ([20000, 17], 1, 8, 2, 128, 1, 0, "nhd", 0.0, True),
+    # and rows that do not: one head a wavefront on the same tables
+    ([700, 33], 1, 18, 2, 128, 16, 0, "nhd", 0.0, False),
+    ([700, 33], 1, 3, 3, 128, 64, 0, "nhd", 0.0, False),
+    ([700, 1033], 5, 32, 8, 128, 32, 600, "hnd", 0.0, False),
+]
+
+
+@pytest.mark.parametrize("lens,Q,Hq,Hkv,D,page,window,order,cap,bias", WIDE_CASES)
+def test_wide_tables(lens, Q, Hq, Hkv, D, page, window, order, cap, bias):
+    say(f"[attn4 wide] lens={lens[:8]} x{len(lens)} Q={Q} Hq={Hq} Hkv={Hkv} D={D} page={page} "
+        f"window={window} {order} cap={cap} bias={bias}")
+    q, table, ln, parts = build4(lens, Q, Hq, Hkv, D, page, seed=D + page + 1)
+    width = -(-(1 << 18) // (len(lens) * Hkv * page)) + 1
+    table = torch.cat([table, torch.full((len(lens), max(0, width - table.shape[1])), -5,
+                                         dtype=torch.int32)], 1)
+    slopes = slopes_of(Hq) if bias else None
+    got = run(q, place4(parts, order, DEV), table, ln, window=window, softcap=cap,
+              slopes=None if slopes is None else slopes.to(DEV))
+    r = check(got, q, parts, table, ln, None, window, cap, slopes)
+    say(f"  max err / tol = {r:.3f}")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-38, -1e-30])
+@pytest.mark.parametrize("width", [4, 40000])
+def test_scales_of_any_sign(scale, width):
+    """A negative factor turns the order of the keys, zero and the smallest make
+    all that are seen alike; those that are not seen stay out."""
+    q, table, ln, parts = build4([50, 3, 0], 2, 8, 2, 64, 16, seed=21)
+    table = torch.cat([table, torch.full((3, width - table.shape[1] + 4), -1, dtype=torch.int32)], 1)
+    got = run(q, place4(parts, "nhd", DEV), table, ln, scale=scale)
+    check(got, q, parts, table, ln, scale)
+    got = run(q, place4(parts, "nhd", DEV), table, ln, scale=scale, softcap=2.0)
+    check(got, q, parts, table, ln, scale, 0, 2.0)
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 def test_large_and_ascending_scores(D):
     """Scores of hundreds, and scores that grow from key to key: the reference of
@@ -173,14 +224,14 @@ def test_weights_of_24_bits(keys):
 
 @pytest.mark.parametrize("D,page,Q,Hkv", [(64, 16, 3, 2), (128, 5, 3, 2), (128, 16, 1, 1),
                                           (256, 16, 2, 2), (128, 32, 20, 1)])
-@pytest.mark.parametrize("wide", [0, 3000])
+@pytest.mark.parametrize("wide", [0, 3000, 60000])
 def test_what_no_token_sees_does_not_reach_it(D, page, Q, Hkv, wide):
     """NaN scales and other codes behind each sequence, in pages that nobody has
     and before the window leave every row as it was, bit for bit; at the newest
     token they reach its own row only."""
     lens, window = [70, 37, 2], 20
     q, table, ln, parts = build4(lens, Q, 4 * Hkv, Hkv, D, page, seed=9)
-    if wide:   # a wider table: the form for long sequences
+    if wide:   # wider tables: the form for long sequences, with one head a wavefront and two
         table = torch.cat([table, torch.full((3, wide // page), -1, dtype=torch.int32)], 1)
     clean = run(q, place4(parts, "nhd", DEV), table, ln, window=window)
     check(clean, q, parts, table, ln, None, window)
@@ -204,15 +255,21 @@ def test_what_no_token_sees_does_not_reach_it(D, page, Q, Hkv, wide):
             assert torch.isnan(got[Q - 1]).all()
 
 
-def test_nan_scale_stays_in_its_block_and_sequence():
+@pytest.mark.parametrize("wide", [0, 60000])
+def test_nan_scale_stays_in_its_head_and_sequence(wide):
     q, table, ln, parts = build4([1500, 700, 90], 2, 4, 2, 128, 16, seed=11)
+    table = torch.cat([table, torch.full((3, wide // 16), -1, dtype=torch.int32)], 1)
     clean = run(q, place4(parts, "nhd", DEV), table, ln)
     parts[1][1][table[1, 20], 3, 1, 5] = 0x7F            # dims 80 .. 95 of head 1
     got = run(q, place4(parts, "nhd", DEV), table, ln)
     assert torch.equal(got[:2], clean[:2]) and torch.equal(got[4:], clean[4:])
     assert torch.equal(got[2:4, :2], clean[2:4, :2])
     assert torch.isnan(got[2:4, 2:, 80:96]).all()
-    assert torch.equal(got[2:4, 2:, :80], clean[2:4, 2:, :80])
+    # its dimensions, or all of them for those that see it
+    same = got[2:4, 2:] == clean[2:4, 2:]
+    assert torch.all(same | torch.isnan(got[2:4, 2:]))
+    if not wide:
+        assert torch.equal(got[2:4, 2:, :80], clean[2:4, 2:, :80])
 
 
 @pytest.mark.parametrize("page", [16, 6])
@@ -225,6 +282,10 @@ def test_missing_pages_and_lengths(page, D, Q):
     cache = place4(parts, "nhd", DEV)
     got = run(q, cache, table, ln)
     check(got, q, parts, table, ln)
+    assert torch.all(got[2 * Q:] == 0)
+    more = torch.cat([table, torch.full((3, 60000 // page), nb, dtype=torch.int32)], 1)
+    got = run(q, cache, more, ln)                        # the form for long sequences
+    check(got, q, parts, more, ln)
     assert torch.all(got[2 * Q:] == 0)
     ln = torch.tensor([1000000, -5, 0x7FFFFFFF], dtype=torch.int32)
     got = run(q, cache, table, ln)
@@ -248,8 +309,9 @@ def test_no_pages_at_all():
     assert torch.all(out == 0)
 
 
-def test_the_same_bits_whatever_the_workspace_held():
-    q, table, ln, parts = build4([9000, 100, 4000], 1, 32, 8, 128, 16, seed=6)
+@pytest.mark.parametrize("lens", [[9000, 100, 4000], [12000, 100, 4000]])   # a head a wavefront, two
+def test_the_same_bits_whatever_the_workspace_held(lens):
+    q, table, ln, parts = build4(lens, 1, 32, 8, 128, 16, seed=6)
     cache = place4(parts, "nhd", DEV)
     n = nv.paged_attention_workspace_bytes(3, 1, 32, 8, 128)
     dq, dt, dl = q.to(DEV), table.to(DEV), ln.to(DEV)
