@@ -636,11 +636,11 @@ nvfp4_status nvfp4_rope_append(const void* q, int64_t q_stride, const void* k, i
  *                     stride_block + token * stride_token + head * stride_head +
  *                     d / 2, in bits 3..0 for even d, 7..4 for odd d. 16-byte
  *                     aligned, strides (bytes) >= D / 2 and multiples of 16,
- *                     stride_token < 2^26;
+ *                     stride_token < 2^26, stride_block < 2^35;
  *   k_scales, v_scales  E4M3 bytes, that of elements 16 b .. 16 b + 15 at block *
  *                     scale_stride_block + .. + b. 4-byte aligned, strides
  *                     (bytes) >= D / 16 and multiples of 4, scale_stride_token <
- *                     2^26. No two elements or scales may share an address (not
+ *                     2^26, scale_stride_block < 2^33. No two elements or scales may share an address (not
  *                     checked);
  *   k_gscale, v_gscale  device float[1], > 0 and finite (not checked);
  *   D                 a multiple of 64; page, num_blocks as in nvfp4_kv_cache.

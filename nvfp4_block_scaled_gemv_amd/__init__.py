@@ -827,22 +827,21 @@ def rope_append_into(q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cach
     inv_freq fp32 [R / 2] turns the first R elements of each head. q and q_out
     may be None (only append); k, v, slots and the caches may be (only
     rotate)."""
-    c = None if k_cache is None or v_cache is None else \
-        (lambda: _kv_cache(k_cache, v_cache, k_scale, v_scale))
-    _rope_append("nvfp4_rope_append", q, k, v, positions, slots, inv_freq, q_out, c,
-                 (k_cache, v_cache, k_scale, v_scale), interleaved, rope_scale)
-
-
-def _rope_append(fn, q, k, v, positions, slots, inv_freq, q_out, make_cache, parts, interleaved,
-                 rope_scale) -> None:
-    """The call of either append; make_cache gives the cache's descriptor (None:
-    there is no cache), parts are its tensors."""
     x = k if q is None else q
     if x is None:
         raise ValueError("neither q nor k is given")
-    if (k is None) != (v is None) or (k is not None and make_cache is None):
+    if (k is None) != (v is None) or (k is not None and (k_cache is None or v_cache is None)):
         raise ValueError("k, v and the caches go together")
-    _same_device(x.get_device(), q, k, v, positions, slots, inv_freq, q_out, *parts)
+    _same_device(x.get_device(), q, k, v, positions, slots, inv_freq, q_out, k_cache, v_cache,
+                 k_scale, v_scale)
+    c = None if k is None else _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    _rope_append("nvfp4_rope_append", lib().nvfp4_rope_append, x, q, k, v, positions, slots,
+                 inv_freq, q_out, c, interleaved, rope_scale)
+
+
+def _rope_append(name, fn, x, q, k, v, positions, slots, inv_freq, q_out, c, interleaved,
+                 rope_scale) -> None:
+    """The call of either append; x: q or k, c: the cache's descriptor (with k)."""
     xt = _ACT_TYPES.get(x.dtype)
     if xt is None:
         raise TypeError(f"q, k and v must be bf16 or fp32, got {x.dtype}")
@@ -865,7 +864,6 @@ def _rope_append(fn, q, k, v, positions, slots, inv_freq, q_out, make_cache, par
         if T == 1:   # one token's stride says nothing
             qs = Hq * D
     if k is not None:
-        c = make_cache()
         Hkv, st, sv = c.n_kv_heads, k.stride(), v.stride()
         if k.dtype is not x.dtype or v.dtype is not x.dtype or k.shape != (T, Hkv, D) \
                 or v.shape != k.shape or c.D != D:
@@ -880,7 +878,7 @@ def _rope_append(fn, q, k, v, positions, slots, inv_freq, q_out, make_cache, par
         if T == 1:
             ks = vs = Hkv * D
         cache = ctypes.byref(c)
-    _check(fn, getattr(lib(), fn)(
+    _check(name, fn(
         qp, qs or 0, kp, ks or 0, vp, vs or 0, xt, positions.data_ptr(), sp,
         inv_freq.data_ptr(), T, Hq, D, 2 * inv_freq.shape[0], 1 if interleaved else 0,
         rope_scale, op, cache, _stream(x)))
@@ -931,9 +929,15 @@ def rope_append_nvfp4_into(q, k, v, positions, slots, inv_freq, q_out, k_cache, 
     """rope_append_into with an NVFP4 cache: k_cache and v_cache are triples
     (codes u8 [blocks, page, Hkv, D / 2], scales u8 [blocks, page, Hkv, D / 16],
     gscale fp32 [1])."""
-    _rope_append("nvfp4_rope_append_nvfp4", q, k, v, positions, slots, inv_freq, q_out,
-                 lambda: _kv_cache4(k_cache, v_cache), (*k_cache, *v_cache), interleaved,
-                 rope_scale)
+    x = k if q is None else q
+    if x is None:
+        raise ValueError("neither q nor k is given")
+    if (k is None) != (v is None):
+        raise ValueError("k and v go together")
+    _same_device(x.get_device(), q, k, v, positions, slots, inv_freq, q_out, *k_cache, *v_cache)
+    c = _kv_cache4(k_cache, v_cache)
+    _rope_append("nvfp4_rope_append_nvfp4", lib().nvfp4_rope_append_nvfp4, x, q, k, v, positions,
+                 slots, inv_freq, q_out, c, interleaved, rope_scale)
 
 
 def rope_append_nvfp4(q, k, v, positions, slots, inv_freq, k_cache, v_cache,
@@ -958,28 +962,27 @@ def paged_attention_into(q, k_cache, v_cache, block_table, seq_lens, out, worksp
     block_table int32 [B, max_blocks]; seq_lens int32 [B], the new tokens
     included; scale defaults to D ** -0.5; window > 0: each token sees the
     last `window` keys up to itself."""
-    _paged_attention("nvfp4_paged_attention", q, lambda: _kv_cache(k_cache, v_cache, k_scale, v_scale),
-                     (k_cache, v_cache, k_scale, v_scale), block_table, seq_lens, out, workspace,
-                     scale, window)
+    _same_device(q.get_device(), k_cache, v_cache, block_table, seq_lens, out, workspace, k_scale,
+                 v_scale)
+    _paged_attention("nvfp4_paged_attention", lib().nvfp4_paged_attention, q,
+                     _kv_cache(k_cache, v_cache, k_scale, v_scale), block_table, seq_lens, out,
+                     workspace, scale, window)
 
 
-def _paged_attention(fn, q, make_cache, parts, block_table, seq_lens, out, workspace, scale,
-                     window, *scores) -> None:
-    """The call of any attention; make_cache gives the cache's descriptor, parts
-    are its tensors (and the slopes)."""
-    _same_device(q.get_device(), block_table, seq_lens, out, workspace, *parts)
+def _paged_attention(name, fn, q, c, block_table, seq_lens, out, workspace, scale, window,
+                     *scores) -> None:
+    """The call of any attention; c: the cache's descriptor."""
     if q.dtype is not torch.bfloat16 or out.dtype is not torch.bfloat16 \
             or block_table.dtype is not torch.int32 or seq_lens.dtype is not torch.int32:
         raise TypeError("q and out must be bf16, block_table and seq_lens int32")
     _contiguous(q, out, block_table, seq_lens, workspace)
-    c = make_cache()
     T, Hq, D = q.shape
     B, width = block_table.shape
     if seq_lens.shape != (B,) or out.shape != q.shape or D != c.D or (T % B if B else T):
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, out {tuple(out.shape)}, "
                          f"block_table {tuple(block_table.shape)}, seq_lens "
                          f"{tuple(seq_lens.shape)}, D {c.D}")
-    _check(fn, getattr(lib(), fn)(
+    _check(name, fn(
         q.data_ptr(), ctypes.byref(c), block_table.data_ptr(), seq_lens.data_ptr(), B,
         T // B if B else 0, Hq, width, D ** -0.5 if scale is None else scale, window, *scores,
         out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(q)))
@@ -1022,9 +1025,10 @@ def paged_attention_scored_into(q, k_cache, v_cache, block_table, seq_lens, out,
     """paged_attention_into with scores z capped (softcap > 0: softcap * tanh(z /
     softcap)), then biased by distance (slopes fp32 [Hq]: + slopes[h] * (key -
     token's position))."""
-    _paged_attention("nvfp4_paged_attention_scored", q,
-                     lambda: _kv_cache(k_cache, v_cache, k_scale, v_scale),
-                     (k_cache, v_cache, k_scale, v_scale, slopes), block_table, seq_lens, out,
+    _same_device(q.get_device(), k_cache, v_cache, block_table, seq_lens, out, workspace, k_scale,
+                 v_scale, slopes)
+    _paged_attention("nvfp4_paged_attention_scored", lib().nvfp4_paged_attention_scored, q,
+                     _kv_cache(k_cache, v_cache, k_scale, v_scale), block_table, seq_lens, out,
                      workspace, scale, window, _scores(softcap, slopes, q.shape[1]))
 
 
@@ -1043,8 +1047,9 @@ def paged_attention_nvfp4_into(q, k_cache, v_cache, block_table, seq_lens, out, 
     """paged_attention_into over an NVFP4 cache (the triples of
     rope_append_nvfp4_into), with the cap and bias of
     paged_attention_scored_into."""
-    _paged_attention("nvfp4_paged_attention_nvfp4", q, lambda: _kv_cache4(k_cache, v_cache),
-                     (*k_cache, *v_cache, slopes), block_table, seq_lens, out, workspace, scale,
+    _same_device(q.get_device(), block_table, seq_lens, out, workspace, slopes, *k_cache, *v_cache)
+    _paged_attention("nvfp4_paged_attention_nvfp4", lib().nvfp4_paged_attention_nvfp4, q,
+                     _kv_cache4(k_cache, v_cache), block_table, seq_lens, out, workspace, scale,
                      window, _scores(softcap, slopes, q.shape[1]))
 
 

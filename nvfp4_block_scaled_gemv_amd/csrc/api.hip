@@ -571,8 +571,8 @@ nvfp4_status cache4_checks(const char* fn, const nvfp4_kv_cache4& c) {
   const int64_t far = 1LL << 40;
   if (c.num_blocks > 0x7FFFFFFF || c.page > (1 << 20) || c.n_kv_heads > NVFP4_MAX_HEADS ||
       c.D > NVFP4_ROPE_MAX_D || c.stride_token >= (1 << 26) ||
-      c.scale_stride_token >= (1 << 26) || c.stride_head >= far || c.stride_block >= far ||
-      c.scale_stride_head >= far || c.scale_stride_block >= far ||
+      c.scale_stride_token >= (1 << 26) || c.stride_head >= far || c.stride_block >= 1LL << 35 ||
+      c.scale_stride_head >= far || c.scale_stride_block >= 1LL << 33 ||
       (__int128)c.num_blocks * c.stride_block >= (1LL << 58) ||
       (__int128)c.num_blocks * c.scale_stride_block >= (1LL << 58))
     return fail(NVFP4_ERR_UNSUPPORTED,

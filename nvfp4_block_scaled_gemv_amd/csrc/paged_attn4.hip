@@ -176,7 +176,8 @@ struct Attn4Wave
     }
   }
   __device__ __forceinline__ void place(int u, int id, int in) {
-    // a page's stride is a multiple of 16 below 2^35: products of 32 bits
+    // a page's stride is a multiple of 16 below 2^35 (its scales' one of 4 below
+    // 2^33): products of 32 bits
     off[u] = (int64_t)((uint64_t)(uint32_t)id * (uint32_t)(a.sb >> 4)) * 16 +
              (int64_t)((uint64_t)(uint32_t)in * st) + head_off;
     boff[u] = alike ? off[u] >> 3

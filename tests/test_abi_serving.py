@@ -44,9 +44,9 @@ BAD_CACHES = [
     (dict(stride_head=-32), ERR_SHAPE), (dict(nb=1 << 31), ERR_UNSUPPORTED),
     (dict(page=(1 << 20) + 1), ERR_UNSUPPORTED), (dict(heads=1025), ERR_UNSUPPORTED),
     (dict(stride_token=1 << 26), ERR_UNSUPPORTED), (dict(scale_stride_token=1 << 26), ERR_UNSUPPORTED),
-    (dict(stride_block=1 << 40), ERR_UNSUPPORTED), (dict(stride_head=1 << 40), ERR_UNSUPPORTED),
+    (dict(stride_block=1 << 35), ERR_UNSUPPORTED), (dict(stride_head=1 << 40), ERR_UNSUPPORTED),
     (dict(scale_stride_head=1 << 40), ERR_UNSUPPORTED),
-    (dict(scale_stride_block=1 << 40), ERR_UNSUPPORTED),
+    (dict(scale_stride_block=1 << 33), ERR_UNSUPPORTED),
     (dict(nb=1 << 30, stride_block=1 << 29), ERR_UNSUPPORTED),
     (dict(k=None), ERR_NULL), (dict(vs=None), ERR_NULL), (dict(kg=None), ERR_NULL),
     (dict(vg=None, nb=0), ERR_NULL), (dict(v=A[8]), ERR_NULL), (dict(vs=A[10]), ERR_NULL),
