@@ -742,7 +742,7 @@ nvfp4_status nvfp4_paged_attention(const uint16_t* q, const nvfp4_kv_cache* cach
  *   z = softcap * tanh(z / softcap)     (softcap > 0)
  *   z = z + slopes[head] * (j - p)      (slopes != NULL)
  *
- *   softcap  0 (none) or 1e-6 .. 1e30; tanh is within 2^-22 of its value;
+ *   softcap  0 (none) or 1e-6 .. 1e30; tanh is within 2^-21 of its value;
  *   slopes   device float[Hq], finite (not checked), or NULL. Positive slopes
  *            weigh far keys less.
  * The structure is read on the host during the call.

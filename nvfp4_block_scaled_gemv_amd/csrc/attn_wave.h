@@ -131,17 +131,22 @@ __device__ __forceinline__ uint32_t perm_lo(uint32_t a, uint32_t b) {   // halve
 __device__ __forceinline__ uint32_t perm_hi(uint32_t a, uint32_t b) {   // halves 1 of a, b
   return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
-// tanh to 2^-22 of it: the odd series up to 0.3 (its next term is 2^-24 there),
-// then 1 - 2 / (exp(2 x) + 1), which is 1 where the exponential overflows. The
-// series takes over where the second form's rounding, 2^-24 of one, would show.
-__device__ __forceinline__ float tanh_32(float x) {
-  const float y = fabsf(x), s = x * x;
-  const float big = fmaf(-2.0f, __builtin_amdgcn_rcpf(__builtin_amdgcn_exp2f(y * (2.0f * kLog2e)) + 1.0f), 1.0f);
-  float p = fmaf(s, 62.0f / 2835.0f, -17.0f / 315.0f);
-  p = fmaf(s, p, 2.0f / 15.0f);
-  p = fmaf(s, p, -1.0f / 3.0f);
-  p = fmaf(s * y, p, y);
-  return copysignf(y < 0.3f ? p : big, x);
+// tanh to 2^-21 of it. Up to 1.25 a quotient of its continued fraction, x (10395 +
+// 1260 s + 21 s^2) / (10395 + 4725 s + 210 s^2 + s^3) with s = x^2, off by 2^-27 at
+// most; beyond, 1 - 2 / (exp(2 x) + 1), which is 1 where the exponential overflows
+// (below, its rounding, 2^-24 of one, would show).
+constexpr float kTanhNear = 1.25f;
+__device__ __forceinline__ float tanh_near(float x) {
+  const float s = x * x;
+  const float n = fmaf(fmaf(s, 21.0f, 1260.0f), s, 10395.0f);
+  const float d = fmaf(fmaf(s + 210.0f, s, 4725.0f), s, 10395.0f);
+  return x * n * __builtin_amdgcn_rcpf(d);
+}
+__device__ __forceinline__ float tanh_any(float x) {
+  const float y = fabsf(x);
+  const float e = __builtin_amdgcn_exp2f(y * (2.0f * kLog2e));
+  const float far = fmaf(-2.0f, __builtin_amdgcn_rcpf(e + 1.0f), 1.0f);
+  return y <= kTanhNear ? tanh_near(x) : copysignf(far, x);
 }
 
 // LDS is written and read by the lanes of one wavefront, in order: the compiler
@@ -265,11 +270,20 @@ struct AttnPass {
   __device__ __forceinline__ void modify(f32x4_t (&S)[RT][NU], const Cursor& cur) {
     if (a.softcap > 0.0f) {
       const float to = a.softcap * kLog2e;
+      float top = 0.0f;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int e = 0; e < 4 * NU; ++e)
-          S[rt][e >> 2][e & 3] = to * tanh_32(S[rt][e >> 2][e & 3]);
+        for (int e = 0; e < 4 * NU; ++e) top = fmaxf(top, fabsf(S[rt][e >> 2][e & 3]));
+      // most tiles of scores that a cap of tens is meant for hold none far out
+      const bool far = __any(top > kTanhNear);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int e = 0; e < 4 * NU; ++e) {
+          const float x = S[rt][e >> 2][e & 3];
+          S[rt][e >> 2][e & 3] = to * (far ? tanh_any(x) : tanh_near(x));
+        }
     }
     if (a.slopes) {
 #pragma unroll
@@ -277,7 +291,8 @@ struct AttnPass {
         const int from = cur.key - (cur.len - Q + tok[rt]);
 #pragma unroll
         for (int e = 0; e < 4 * NU; ++e)
-          S[rt][e >> 2][e & 3] = fmaf(slope[rt], (float)(from + W::key_of(e, g)), S[rt][e >> 2][e & 3]);
+          S[rt][e >> 2][e & 3] =
+              fmaf(slope[rt], (float)(from + W::key_of(e, g)), S[rt][e >> 2][e & 3]);
       }
     }
   }

@@ -22,8 +22,8 @@ def run(q, cache, table, lens, **kw):
 
 def check(got, q, parts, table, lens, scale=None, window=0, softcap=0.0, slopes=None):
     """The bound. Scores: D exact products summed in fp32, off by at most 2 D
-    2^-24 |q| |k| scale and 2^-23 of themselves for the scale's products; the cap
-    adds 2^-21 of them, the bias 2^-23 of its size and of the score's. q enters
+    2^-24 |q| |k| scale; the cap adds 2^-21 of them, the scale's products, the bias
+    and the factors of log2 six roundings of 2^-24: 2^-20 of the largest in all. q enters
     within 2^-39 of its largest element, far below the sums' 2^-24. A weight is
     off by twice the score's error and 2^-24 (its two fp16), or 2^-36 of the
     row's largest: sum_j 2^-36 |v_j| in all, the sum of weights being at least
@@ -40,7 +40,7 @@ def check(got, q, parts, table, lens, scale=None, window=0, softcap=0.0, slopes=
     ref = attention(q, k, v, table, lens, scale, window, softcap, slopes, weigh)
     a = attention(q, k, v.abs(), table, lens, scale, window, softcap, slopes)
     size = float(q.double().norm(dim=-1).max() * k.norm(dim=-1).max()) * abs(scale)
-    dz = 2 * D * 2.0 ** -24 * size + 2.0 ** -21 * top[0]
+    dz = 2 * D * 2.0 ** -24 * size + 2.0 ** -20 * top[0]
     n = min(int(lens.max()), table.shape[1] * parts[0][0].shape[1])
     tol = a * (2 * dz + 2.0 ** -24 + 2.0 ** -14) + n * 2.0 ** -36 * float(v.abs().max()) \
         + ref.abs() * 2.0 ** -8 + 1e-30
@@ -352,3 +352,25 @@ def test_windows_at_the_end(page, D, window):
         ln = torch.tensor([n], dtype=torch.int32)
         got = run(q, place4(parts, "nhd", DEV), table, ln, window=window)
         check(got, q, parts, table, ln, None, window)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("width", [0, 20000])
+def test_far_strides(D, width):
+    """Tokens and heads hundreds of kilobytes to 32 MB apart: a tile's offsets come
+    near 2^32 bytes."""
+    q, table, ln, parts = build4([61], 2, 4, 2, D, 16, seed=31, spare=0)
+    table = torch.cat([table, torch.full((1, width), -1, dtype=torch.int32)], 1)
+    nb = parts[0][0].shape[0]
+    cache = []
+    for c, s, g in parts:
+        far = []
+        for x, token in ((c, 1 << 25), (s, (1 << 25) - 64)):
+            n = x.shape[-1]
+            raw = torch.empty(16 * token + 2 * 300000 * 16, dtype=torch.uint8, device=DEV)
+            view = torch.as_strided(raw, (nb, 16, 2, n), (4096, token, 300000 * 16, 1))
+            view.copy_(x)
+            far.append(view)
+        cache.append((*far, torch.full((1,), g, device=DEV)))
+    got = run(q, cache, table, ln)
+    check(got, q, parts, table, ln)

@@ -21,9 +21,9 @@ def run(q, table, lens, kc, vc, ks, vs, ct, slopes=None, **kw):
 
 
 def check(got, q, k, v, table, lens, scale, window, ks, vs, softcap, slopes):
-    """The bound of plain attention over these caches, with scores off by 2^-21 of
-    their largest more: the scale's products, the cap (2^-22 of it) and the bias
-    (its product and its addition, 2^-24 each) and the factors of log2."""
+    """The bound of plain attention over these caches, with scores off by 2^-20 of
+    their largest more: the cap (2^-21 of it), and six roundings of 2^-24 for the
+    scale's products, the bias's product and addition and the factors of log2."""
     top = [0.0]
 
     def weigh(z, w, vh):
@@ -33,7 +33,7 @@ def check(got, q, k, v, table, lens, scale, window, ks, vs, softcap, slopes):
     a = attention(q, kd, vd.abs(), table, lens, scale, window, softcap, slopes)
     D = q.shape[-1]
     size = float(q.double().norm(dim=-1).max() * kd.norm(dim=-1).max()) * abs(scale)
-    dz = 2 * D * 2.0 ** -24 * size + 2.0 ** -21 * top[0]
+    dz = 2 * D * 2.0 ** -24 * size + 2.0 ** -20 * top[0]
     tol = a * (2.0 ** -23 + 2 * dz + 2.0 ** -14) + ref.abs() * 2.0 ** -8 + 1e-30
     err = (got - ref).abs()
     bad = ~(err <= tol)
@@ -112,3 +112,13 @@ def test_a_cap_makes_infinite_scores_finite():
     k[table[0, 0], 3, 0, 0] = float("nan")
     kc.copy_(k)
     assert torch.isnan(run(q, table, ln, kc, vc, ks, vs, BF16, softcap=10.0)).all()
+
+
+@pytest.mark.parametrize("cap,spread", [(50.0, 1.0), (50.0, 9.0), (2.0, 9.0), (500.0, 60.0)])
+def test_tanh_near_and_far(cap, spread):
+    """Tiles whose scores all lie in tanh's near part, in both, and far out, against
+    a weighted mean that shows the scores' errors: 2^-21 of the cap at most."""
+    q, k, v, table, ln, kc, vc, ks, vs = build([300], 1, 4, 1, 64, 16, BF16, seed=15)
+    q = q * spread
+    got = run(q, table, ln, kc, vc, ks, vs, BF16, softcap=cap)
+    check(got, q, k, v, table, ln, 0.125, 0, ks, vs, cap, None)
