@@ -640,8 +640,8 @@ nvfp4_status nvfp4_rope_append(const void* q, int64_t q_stride, const void* k, i
  *   k_scales, v_scales  E4M3 bytes, that of elements 16 b .. 16 b + 15 at block *
  *                     scale_stride_block + .. + b. 4-byte aligned, strides
  *                     (bytes) >= D / 16 and multiples of 4, scale_stride_token <
- *                     2^26, scale_stride_block < 2^33. No two elements or scales may share an address (not
- *                     checked);
+ *                     2^26, scale_stride_block < 2^33. No two elements or
+ *                     scales may share an address (not checked);
  *   k_gscale, v_gscale  device float[1], > 0 and finite (not checked);
  *   D                 a multiple of 64; page, num_blocks as in nvfp4_kv_cache.
  * The structure is read on the host during the call.
@@ -831,8 +831,8 @@ size_t nvfp4_lora_workspace_bytes(int64_t M, int64_t K, int64_t rank, int64_t n_
  *   workspace   at least nvfp4_lora_workspace_bytes(M, K, rank, n_segments)
  *               bytes, 256-byte aligned; overwritten, its content does not
  *               matter; must not be shared by calls that may run concurrently.
- * base may be its own segment's y; no output may overlap anything else. Two
- * launches. Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, WORKSPACE, ALIAS, HIP.
+ * base may be its own segment's y; no output may overlap anything else. One or
+ * two launches. Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, WORKSPACE, ALIAS, HIP.
  */
 nvfp4_status nvfp4_lora_segments(const nvfp4_lora_segment* segs, int64_t n_segments,
                                  int64_t n_adapters, int64_t rank, const int32_t* ids,

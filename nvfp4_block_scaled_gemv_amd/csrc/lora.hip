@@ -32,14 +32,18 @@ constexpr int kStep = 32;          // inputs per matrix instruction
 constexpr int kDeep = 8;           // of them per wavefront and turn
 constexpr int kTurn = 4 * kDeep * kStep;   // inputs of a workgroup's turn: 1024
 constexpr int kMaxChunks = 16;
-constexpr int kOuts = 256;         // outputs per workgroup of k_lora_up
+// Outputs per workgroup of k_lora_up. One, two or four blocks of 256 (the next one's
+// loads before one's outputs are stored), both kernels, us: 16 sequences of 8 rows,
+// rank 32 13.9 / 16.5 / 16.0; 128 rows of as many adapters, 6144 outputs, rank 16 26.2 /
+// 25.2 / 23.8, of one adapter 13.0 / 14.0 / 16.2; 48 rows of 38 adapters of ranks 16
+// to 64, 24576 outputs 44.5 / 44.1 / 45.4.
+constexpr int kOuts = 256;
 constexpr int kAllOuts = 1024;     // and of k_lora_all
 
 struct LoraShape {
   int chunks, turns;               // chunks of K, turns of a chunk
   int tiles;                       // tiles of 16 ranks
   int blocks;                      // workgroups per row of k_lora_up, k_lora_all
-  int outs;                        // outputs of one
   float* t;                        // [chunks][segments][M][rank]
 };
 
@@ -81,6 +85,19 @@ __device__ __forceinline__ Rows rows_of(const LoraArgs& a, int m, int (&list)[16
   return r;
 }
 
+// The row of a workgroup (M and more: none). From 16 rows on they start in the order
+// 0 8 16 .., 4 12 .., 2 10 .., 6 .., 1 .., 5 .., 3 .., 7 ..: where a request has
+// several rows, which are neighbours as a rule, those that begin a group start
+// early, and the workgroups that have nothing to do, of 1 us each, late. Rows in
+// turn against this, us: 16 sequences of 8 rows, K 12288, 4096 outputs, rank 32 22.9 /
+// 16.7 (the 16 adapters in turn over the rows 16.7 / 21.9); 128 rows of one adapter,
+// 6144 outputs 18.5 / 14.1, of as many 25.3 / 25.2; 48 rows of 38, 24576 outputs
+// 42.3 / 44.1.
+__device__ __forceinline__ int row_of_block() {
+  const int z = blockIdx.z;
+  return blockIdx.y * gridDim.z + ((z & 1) * 4 + (z & 2) + (z >> 2));
+}
+
 // A wavefront's sum over kDeep steps of K from k on: of ranks (columns g * 4 + i of
 // the result) and rows (n). A, X: the lane's row of either at its 8 inputs.
 __device__ __forceinline__ f32x4_t down_step(const uint16_t* A, const uint16_t* X, int64_t k,
@@ -103,7 +120,8 @@ __device__ __forceinline__ f32x4_t down_step(const uint16_t* A, const uint16_t* 
 __global__ __launch_bounds__(kThreads) void k_lora_down(const LoraArgs a, const LoraShape sh) {
   __shared__ int list[16];
   __shared__ float part[4][16][17];
-  const int m = blockIdx.y;
+  const int m = row_of_block();
+  if (m >= (int)a.M) return;
   const Rows rows = rows_of(a, m, list);
   if (rows.count == 0 || rows.id < 0) return;
   int u = blockIdx.x;
@@ -156,7 +174,7 @@ struct Up {
   const LoraSegment& s;
   const uint16_t* const B;
   const int rank, c, g;
-  int64_t n0;
+  const int64_t n0;
   u32x4_t w[2][G];                     // two steps of 8 G ranks
   f32x4_t y[4];                        // base of the lane's rows g * 4 + i
 
@@ -216,52 +234,38 @@ struct Up {
                                                          acc[j], 0, 0, 0);
     }
   }
-  // After load() of steps 0 and 1 (where there is one) and load_base(): these 64
-  // outputs, and those `stride` further below `end`.
+  // After load() of steps 0 and 1 (where there is one) and load_base().
   __device__ __forceinline__ void finish(int own, float alpha, const uint16_t* lds_t,
-                                         const int* list, int count, int stride, int64_t end) {
+                                         const int* list, int count) {
     const int ld = lds_row(rank), steps = (own + 8 * G - 1) / (8 * G);
-    int64_t first = n0 - c * 4;        // uniform
-    for (;;) {
-      f32x4_t acc[4];
+    f32x4_t acc[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-      if (G < 4) {                     // one step
-        if (steps) multiply(w[0], 0, own, lds_t, ld, acc);
+    for (int j = 0; j < 4; ++j) acc[j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    if (G < 4) {                       // one step
+      if (steps) multiply(w[0], 0, own, lds_t, ld, acc);
+    } else {
+      for (int i = 0; i < steps; i += 2) {
+        multiply(w[0], i, own, lds_t, ld, acc);
+        if (i + 2 < steps) load(i + 2, w[0]);
+        if (i + 1 < steps) multiply(w[1], i + 1, own, lds_t, ld, acc);
+        if (i + 3 < steps) load(i + 3, w[1]);
+      }
+    }
+    // acc[j][i]: row g * 4 + i, output n0 + j
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (g * 4 + i >= count || n0 >= s.N) continue;
+      float* p = s.y + (int64_t)list[g * 4 + i] * s.N + n0;
+      f32x4_t v;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = fmaf(alpha, acc[j][i], y[i][j]);
+      if (s.wide) {
+        *reinterpret_cast<f32x4_t*>(p) = v;
       } else {
-        for (int i = 0; i < steps; i += 2) {
-          multiply(w[0], i, own, lds_t, ld, acc);
-          if (i + 2 < steps) load(i + 2, w[0]);
-          if (i + 1 < steps) multiply(w[1], i + 1, own, lds_t, ld, acc);
-          if (i + 3 < steps) load(i + 3, w[1]);
-        }
-      }
-      const int64_t at = n0;
-      first += stride;
-      const bool more = first < end;
-      if (more) {                      // the next ones' loads before these are stored
-        n0 += stride;
-        load(0, w[0]);
-        if (G == 4 && steps > 1) load(1, w[1]);
-      }
-      // acc[j][i]: row g * 4 + i, output at + j
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (g * 4 + i >= count || at >= s.N) continue;
-        float* p = s.y + (int64_t)list[g * 4 + i] * s.N + at;
-        f32x4_t v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = fmaf(alpha, acc[j][i], y[i][j]);
-        if (s.wide) {
-          *reinterpret_cast<f32x4_t*>(p) = v;
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (at + j < s.N) p[j] = v[j];
-        }
+        for (int j = 0; j < 4; ++j)
+          if (n0 + j < s.N) p[j] = v[j];
       }
-      if (!more) break;
-      load_base(list, count);
     }
   }
 };
@@ -286,13 +290,14 @@ template <int G>
 __global__ __launch_bounds__(kThreads) void k_lora_up(const LoraArgs a, const LoraShape sh) {
   __shared__ int list[16];
   extern __shared__ __align__(16) uint16_t lds_t[];
-  const int m = blockIdx.y;
+  const int m = row_of_block();
+  if (m >= (int)a.M) return;
   const Rows rows = rows_of(a, m, list);
   if (rows.count == 0) return;
   int block = blockIdx.x, seg = 0;
   while (block >= a.segs[seg].blocks) block -= a.segs[seg++].blocks;
   const LoraSegment& s = a.segs[seg];
-  const int64_t first = (int64_t)block * sh.outs, end = first + sh.outs < s.N ? first + sh.outs : s.N;
+  const int64_t first = (int64_t)block * kOuts, end = first + kOuts < s.N ? first + kOuts : s.N;
   if (rows.id < 0) return copy_base(s, list, rows.count, first, end);
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rank = (int)a.rank;
   Up<G> up(s, rows.id, rank, first + wv * 64);
@@ -316,7 +321,7 @@ __global__ __launch_bounds__(kThreads) void k_lora_up(const LoraArgs a, const Lo
     put_t(lds_t, ld, tn, tr, v);
   }
   __syncthreads();
-  up.finish(own, alpha, lds_t, list, rows.count, 256, end);
+  up.finish(own, alpha, lds_t, list, rows.count);
 }
 
 // All in one: 16 wavefronts, each 64 outputs; of t they take 256 inputs each in
@@ -332,7 +337,8 @@ __global__ __launch_bounds__(1024) void k_lora_all(const LoraArgs a, const LoraS
   int block = blockIdx.x, seg = 0;
   while (block >= a.segs[seg].blocks) block -= a.segs[seg++].blocks;
   const LoraSegment& s = a.segs[seg];
-  const int64_t first = (int64_t)block * sh.outs, end = first + sh.outs < s.N ? first + sh.outs : s.N;
+  const int64_t first = (int64_t)block * kAllOuts;
+  const int64_t end = first + kAllOuts < s.N ? first + kAllOuts : s.N;
   if (rows.id < 0) return copy_base(s, list, rows.count, first, end);
   const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), rank = (int)a.rank;
@@ -365,7 +371,7 @@ __global__ __launch_bounds__(1024) void k_lora_all(const LoraArgs a, const LoraS
   up.load_base(list, rows.count);
   if (G == 4 && own > 32) up.load(1, up.w[1]);
   __syncthreads();
-  up.finish(own, alpha, lds_t, list, rows.count, 1024, end);
+  up.finish(own, alpha, lds_t, list, rows.count);
 }
 
 // K in chunks of whole turns, kMaxChunks at most.
@@ -387,18 +393,6 @@ bool all_in_one(const LoraArgs& a, const LoraShape& sh) {
   return a.rank * a.K <= 1 << 16 && a.M * blocks <= 192;
 }
 
-// Outputs of a workgroup of k_lora_up: two blocks of 256 where there are many, for
-// fewer starts (ids, sums, first loads). One, two or four blocks, both kernels, us:
-// 128 rows of as many adapters, 6144 outputs, rank 16 27.1 / 25.5 / 24.3; 48 rows of 38
-// adapters of ranks 16 to 64, 24576 outputs 42.7 / 42.4 / 44.0; 128 rows of one adapter
-// 16.2 / 17.6 / 18.8.
-int outs_of(const LoraArgs& a) {
-  int64_t blocks = 0;
-  for (int s = 0; s < a.n_segments; ++s) blocks += (a.segs[s].N + kOuts - 1) / kOuts;
-  const int64_t each = a.M * blocks / 1024;
-  return kOuts * (int)(each < 1 ? 1 : each > 2 ? 2 : each);
-}
-
 }  // namespace
 
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t rank, int64_t n_segments) {
@@ -413,24 +407,26 @@ hipError_t launch_lora(LoraArgs& a, hipStream_t stream) {
   sh.tiles = (int)((a.rank + 15) / 16);
   sh.t = (float*)a.workspace;
   const bool one = all_in_one(a, sh);
-  sh.outs = one ? kAllOuts : outs_of(a);
+  const int outs = one ? kAllOuts : kOuts;   // of a workgroup
   sh.blocks = 0;
   for (int s = 0; s < a.n_segments; ++s) {
     LoraSegment& g = a.segs[s];
-    g.blocks = (int)((g.N + sh.outs - 1) / sh.outs);
+    g.blocks = (int)((g.N + outs - 1) / outs);
     g.wide = g.N % 4 == 0 && (((uintptr_t)g.y | (uintptr_t)g.base) & 15) == 0;
     sh.blocks += g.blocks;
   }
   if (sh.blocks == 0) return hipSuccess;
+  // (row_of_block's)
+  const uint32_t eighths = a.M >= 16 ? 8 : 1, rows = ((uint32_t)a.M + eighths - 1) / eighths;
   if (!one && sh.chunks && a.n_adapters) {   // without inputs, or adapters, the sums are empty
     hipLaunchKernelGGL(k_lora_down,
-                       dim3((uint32_t)(a.n_segments * sh.tiles * sh.chunks), (uint32_t)a.M),
+                       dim3((uint32_t)(a.n_segments * sh.tiles * sh.chunks), rows, eighths),
                        dim3(kThreads), 0, stream, a, sh);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   const size_t lds = (size_t)3 * 16 * ((a.rank + 31) / 32 * 32 + 8) * sizeof(uint16_t);
-  const dim3 grid((uint32_t)sh.blocks, (uint32_t)a.M), block(one ? 1024 : kThreads);
+  const dim3 grid((uint32_t)sh.blocks, one ? (uint32_t)a.M : rows, one ? 1 : eighths), block(one ? 1024 : kThreads);
   const auto kernel = a.rank == 8    ? (one ? k_lora_all<1> : k_lora_up<1>)
                       : a.rank == 16 ? (one ? k_lora_all<2> : k_lora_up<2>)
                                      : (one ? k_lora_all<4> : k_lora_up<4>);
