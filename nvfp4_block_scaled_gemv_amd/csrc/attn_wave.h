@@ -172,14 +172,14 @@ struct Cursor {
 // their rows fit): the 16 columns of a tile of rows are then HEADS blocks.
 // MOD: the scores are capped or biased. W::kStage: bytes of LDS that a wavefront
 // takes V through (0: none), in W::take_v().
-template <class W, int TILE, int RT, int RUN, bool MOD, int HEADS = 1>
+template <class W, int TILE, int RT, int RUN, bool MOD, int HEADS = 1, int NU_ = TILE / 16>
 struct AttnPass {
   static_assert(HEADS == 1 || RT == 1, "heads side by side: one tile of rows");
   static constexpr int kTile = TILE;
   static constexpr int kHeads = HEADS;
   static constexpr int kCols = 16 / HEADS;     // columns per head
   static constexpr int kRT = RT;
-  static constexpr int NU = TILE / 16;         // runs of 16 keys
+  static constexpr int NU = NU_;               // a lane's scores: words of four
   static constexpr int NO = RUN ? TILE / RUN : 1;
   typedef typename std::conditional<TILE == 64, uint64_t, uint32_t>::type Mask;   // bit per key
   static constexpr Mask kAll = ~(Mask)0;
@@ -346,6 +346,15 @@ struct AttnPass {
           }
         }
       }
+      // all of a lane's scores may be of another head than its row's
+      if constexpr (W::kOthers) {
+        const bool other = (g & 1) != hl;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+          for (int e = 0; e < 4 * NU; ++e)
+            S[rt][e >> 2][e & 3] = other ? -INFINITY : S[rt][e >> 2][e & 3];
+      }
       w.softmax(S, pf);
       w.take_v();
       if (W::kStage) w.load_v(more);   // V is in LDS: its registers are free
@@ -354,7 +363,7 @@ struct AttnPass {
         const int last = cur.len - Q + t1;
         const int64_t firsts = a.window ? (int64_t)cur.len - Q + t0 - a.window + 1 : 0;
 #pragma unroll
-        for (int e = 0; e < TILE / 4; ++e) {
+        for (int e = 0; e < 4 * NU; ++e) {
           const int key = cur.key + W::key_of(e, g);
           w.keep(e, key <= last && key >= firsts && ((ok_now >> W::key_of(e, g)) & 1u));
         }
@@ -364,7 +373,10 @@ struct AttnPass {
       if constexpr (HEADS > 1) {
         if (w.any_nan()) {
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) weightless[rt] = all ? 0u : weightless[rt];
+          for (int rt = 0; rt < RT; ++rt) {
+            weightless[rt] = all ? 0u : weightless[rt];
+            if (W::kOthers && (g & 1) != hl) weightless[rt] = ~0u;
+          }
           w.settle(weightless);
         }
       }

@@ -101,12 +101,18 @@ struct VRow {
   }
 };
 
-// K, V and O of one wavefront's pass over tiles of one head.
-template <int D, bool FP8, int RT, bool PG, bool MOD>
-struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD>, TK, RT, PG ? 16 : 0, MOD> {
-  using Pass = AttnPass<AttnWave, TK, RT, PG ? 16 : 0, MOD>;
+// K, V and O of one wavefront's pass over tiles of one head, or of two side by
+// side (E4M3): of a tile's 32 rows of K and V, slots, those of quads 0 and 2 of
+// each 16 are then the first head's, of 1 and 3 the second's, at the same keys. A
+// load takes both heads of a key, and a lane's scores are all of one head.
+template <int D, bool FP8, int RT, bool PG, bool MOD, int HEADS = 1>
+struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD, HEADS>, TK / HEADS, RT, PG ? 16 : 0, MOD,
+                           HEADS, TK / 16> {
+  using Pass = AttnPass<AttnWave, TK / HEADS, RT, PG ? 16 : 0, MOD, HEADS, TK / 16>;
   using Pass::a, Pass::sh, Pass::n, Pass::g, Pass::h, Pass::Q, Pass::G, Pass::row0, Pass::c,
-      Pass::tok, Pass::m, Pass::l, Pass::NU, Pass::NO;
+      Pass::tok, Pass::m, Pass::l, Pass::hl, Pass::col, Pass::NU, Pass::NO;
+  static_assert(HEADS == 1 || (FP8 && RT == 1 && D == 64), "any_nan, load_v");
+  static constexpr bool kOthers = HEADS > 1;
   static constexpr int kD = D;
   static constexpr bool kScaled = FP8;
   static constexpr int kPerSimd = waves_per_simd(RT, D, FP8);
@@ -120,7 +126,7 @@ struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD>, TK, RT, PG ? 16 : 0, M
   typedef u32x4_t Weights[kParts][RT][NP];
 
   const int64_t head_off;
-  const uint32_t stb, k_lane, v_dim, v_lane;
+  const uint32_t stb, shb, k_in, k_lane, v_dim, v_lane;   // bytes
   bf16x8_t qf[RT][NJ];
   f32x4_t O[RT][NV];
   u32x4_t kr[NU][KL];
@@ -130,8 +136,11 @@ struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD>, TK, RT, PG ? 16 : 0, M
   __device__ __forceinline__ AttnWave(const AttnArgs& a_, const AttnShape& sh_, int h_, int row0_,
                                       float k_scale, uint8_t*)
       : Pass(a_, sh_, h_, row0_, k_scale), head_off((int64_t)h_ * a_.sh),
-        stb((uint32_t)a_.st * ES), k_lane((uint32_t)n * stb + (uint32_t)g * 16),
-        v_dim((uint32_t)n * (NV > 8 ? 8 : NV) * ES), v_lane((uint32_t)(g * 4) * stb + v_dim) {
+        stb((uint32_t)a_.st * ES), shb(HEADS == 1 ? 0u : (uint32_t)a_.sh * ES),
+        k_in(head_of(n >> 2) * shb + (uint32_t)g * 16),
+        k_lane((uint32_t)key_at(0, n >> 2, n & 3) * stb + k_in),
+        v_dim(head_of(g) * shb + (uint32_t)n * (NV > 8 ? 8 : NV) * ES),
+        v_lane((uint32_t)key_at(0, g, 0) * stb + v_dim) {
     clear();
   }
   __device__ __forceinline__ void clear() {
@@ -146,10 +155,10 @@ struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD>, TK, RT, PG ? 16 : 0, M
   __device__ __forceinline__ void load_q(int b) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int r = row0 + rt * 16 + n;
+      const int r = row0 + rt * 16 + col;
       const bool live = tok[rt] >= 0;
-      const uint16_t* qp = a.q + ((int64_t)(b * (int64_t)Q + (live ? tok[rt] : 0)) * a.Hq + h * G +
-                                  (live ? r - tok[rt] * G : 0)) * D;
+      const uint16_t* qp = a.q + ((int64_t)(b * (int64_t)Q + (live ? tok[rt] : 0)) * a.Hq +
+                                  (h + hl) * G + (live ? r - tok[rt] * G : 0)) * D;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         const int d0 = FP8 ? (j >> 1) * 64 + g * 16 + (j & 1) * 8 : j * 32 + g * 8;
@@ -165,9 +174,18 @@ struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD>, TK, RT, PG ? 16 : 0, M
   __device__ __forceinline__ int64_t at_key(int src) const {
     return this->from_lane(off[0], src) * ES;
   }
+  // slot i of quad `quad` of run u: its key in the tile, and its head from h on
+  static __device__ __forceinline__ int key_at(int u, int quad, int i) {
+    return u * (16 / HEADS) + quad / HEADS * 4 + i;
+  }
+  static __device__ __forceinline__ uint32_t head_of(int quad) {
+    return HEADS == 1 ? 0u : (uint32_t)quad & 1u;
+  }
   // the key of the tile that a lane has as the e-th (of TK / 4) of V, S^T and P
-  static __device__ __forceinline__ int key_of(int e, int g) {
-    return (e >> 2) * 16 + g * 4 + (e & 3);
+  static __device__ __forceinline__ int key_of(int e, int g) { return key_at(e >> 2, g, e & 3); }
+  // run u of 16 slots in its page: two heads' runs share one
+  __device__ __forceinline__ uint32_t run(int u, bool want) const {
+    return HEADS > 1 && want ? (uint32_t)(u * (16 / HEADS)) * stb : 0u;
   }
   // want: false where no tile follows. The loads are issued all the same, all
   // lanes from one address: a branch around them would make the waits on both
@@ -177,8 +195,8 @@ struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD>, TK, RT, PG ? 16 : 0, M
     const uint32_t lane_off = want ? k_lane : 0u;
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
-      const uint8_t* p = PG ? kc + off[PG ? u : 0] * ES + lane_off
-                            : want ? kc + at_key(16 * u + n) + g * 16 : kc;
+      const uint8_t* p = PG ? kc + off[NO > 1 ? u : 0] * ES + run(u, want) + lane_off
+                            : want ? kc + at_key(key_at(u, n >> 2, n & 3)) + k_in : kc;
 #pragma unroll
       for (int j = 0; j < KL; ++j)
         // a load takes 64 bytes of a key: half of an E4M3 head of 128, whose
@@ -190,9 +208,19 @@ struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD>, TK, RT, PG ? 16 : 0, M
   __device__ __forceinline__ void load_v(bool want) {
     const uint8_t* const vc = (const uint8_t*)a.v_cache;
     const uint32_t lane_off = want ? v_lane : 0u, st = want ? stb : 0u;
+    if constexpr (HEADS > 1 && !PG) {   // pages hold whole quads of keys
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        const uint8_t* p = want ? vc + at_key(key_at(u, g, 0)) + v_dim : vc;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vr[u * 4 + i].load(p + (uint32_t)i * st);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < TK / 4; ++i)
-      vr[i].load(PG ? vc + off[PG ? i >> 2 : 0] * ES + (uint32_t)(i & 3) * st + lane_off
+      vr[i].load(PG ? vc + off[NO > 1 ? i >> 2 : 0] * ES + run(i >> 2, want) +
+                          (uint32_t)(i & 3) * st + lane_off
                     : want ? vc + at_key(key_of(i, g)) + v_dim : vc);
   }
 
@@ -295,6 +323,15 @@ struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD>, TK, RT, PG ? 16 : 0, M
 #pragma unroll
     for (int d = 0; d < VRow<NV, FP8>::kDw; ++d) vr[e].w[d] = see ? vr[e].w[d] : 0u;
   }
+  // some value of the tile is NaN (E4M3)
+  __device__ __forceinline__ bool any_nan() const {
+    uint32_t hit = 0u;
+#pragma unroll
+    for (int e = 0; e < TK / 4; ++e)
+#pragma unroll
+      for (int d = 0; d < VRow<NV, FP8>::kDw; ++d) hit |= (vr[e].w[d] & 0x7F7F7F7Fu) + 0x01010101u;
+    return __any((hit & 0x80808080u) != 0u);
+  }
   // A key that some rows see and others do not has weight 0 for these, which is
   // enough unless its value is infinite or NaN (0 * inf would reach them). Such
   // a value becomes zero, and the sum of the rows that see it NaN. weightless:
@@ -362,9 +399,27 @@ int64_t whole_keys(const AttnArgs& a, const AttnShape& sh) {
   if (wgs >= kCus || (wgs >= kCus / 2 && sh.rows >= 16)) return 1024;
   return a.B * a.Q * a.Hq >= 256 && one < 1024 ? 2 * one : one;
 }
-AttnLayout layout(int64_t rows, int64_t Hkv, int64_t D, bool e4m3, bool pg) {
+AttnLayout layout(int64_t rows, int64_t Hkv, int64_t D, bool e4m3, bool pg, int heads = 1) {
   const int RT = row_tiles(rows, D, pg);
-  return attn_layout(rows, Hkv, D, RT, waves_per_simd(RT, (int)D, e4m3));
+  return attn_layout(rows, Hkv, D, RT, waves_per_simd(RT, (int)D, e4m3), heads);
+}
+
+// Two heads of 64 in E4M3 side by side, for scores that are capped or biased (plain
+// ones keep the order of sums that they had): a load then takes whole lines of 128
+// bytes, where each head's 64 come at half of memory's rate, but a wavefront leaves
+// twice the rows to the join. From 2^19 keys of all heads on (by the tables, as
+// the lengths are on the device), and for pages of whole quads of keys, whose places
+// a lane looks up once (with one look-up a key pages of 20 gain nothing). One head
+// against two, us: 16 heads, G 1, pages of 16: 1 sequence of 16384 keys 17.4 /
+// 17.9; 4 of 8192 23.0 / 22.4; 16 of 20000 151 / 119, pages of 20 202 / 161; 8
+// heads, G 4: 4 of 8192 18.1 / 18.3; 16 of 20000 78 / 68; 2 heads, G 8: 16 of 20000
+// 27.4 / 28.5, pages of 20 34.4 / 33.1. A load's bytes have to be counted in 32 bits.
+bool pairs(int64_t rows, int64_t Hkv, int64_t D) { return D == 64 && rows <= 8 && Hkv % 2 == 0; }
+bool side_by_side(const AttnArgs& a, const AttnShape& sh) {
+  return pairs(sh.rows, a.Hkv, a.D) && a.page % 4 == 0 &&
+         a.B * most_keys(a) * a.Hkv >= 1 << 19 && a.sh < 1 << 28 &&
+         most_keys(a) > whole_keys(a, sh) &&
+         (most_keys(a) + 15) / 16 * a.B < 0x7FFFFFFF;   // tiles, as in attn_fits
 }
 
 template <int D, bool FP8, int RT, bool PG, bool MOD>
@@ -377,6 +432,13 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
   const bool pg = a.page % 16 == 0;
   const AttnLayout L = layout(a.Hq / a.Hkv * a.Q, a.Hkv, D, FP8, pg);
   const AttnShape sh = attn_shape(a, L);
+  if constexpr (D == 64 && FP8 && MOD) {
+    if (side_by_side(a, sh)) {
+      const AttnShape two = attn_shape(a, layout(sh.rows, a.Hkv, D, FP8, pg, 2));
+      return pg ? launch_forms<AttnWave<D, FP8, 1, true, MOD, 2>>(a, two, 0, stream)
+                : launch_forms<AttnWave<D, FP8, 1, false, MOD, 2>>(a, two, 0, stream);
+    }
+  }
   if (L.RT == 2) {
     if (pg) return launch_rt<D, FP8, 2, true, MOD>(a, sh, stream);
     if constexpr (D < 256) return launch_rt<D, FP8, 2, false, MOD>(a, sh, stream);
@@ -412,6 +474,10 @@ size_t attn_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv, int64
   size_t most = attn4_workspace_bytes(Hq / Hkv * Q, Hkv, D);
   for (int i = 0; i < 4; ++i) {
     const size_t n = layout(Hq / Hkv * Q, Hkv, D, i & 1, i & 2).total;
+    most = n > most ? n : most;
+  }
+  if (pairs(Hq / Hkv * Q, Hkv, D)) {
+    const size_t n = layout(Hq / Hkv * Q, Hkv, D, true, true, 2).total;
     most = n > most ? n : most;
   }
   return most;

@@ -77,6 +77,7 @@ struct Attn4Wave
       Pass::c, Pass::tok, Pass::m, Pass::l, Pass::hl, Pass::col, Pass::NO;
   static constexpr int kD = D;
   static constexpr bool kScaled = true;
+  static constexpr bool kOthers = false;
   static constexpr int kPerSimd = waves_per_simd(D);
   static constexpr int NU = 4;                 // runs of 16 slots
   static constexpr int E = 16 / HEADS;         // scores that count per lane and row tile

@@ -122,3 +122,72 @@ def test_tanh_near_and_far(cap, spread):
     q = q * spread
     got = run(q, table, ln, kc, vc, ks, vs, BF16, softcap=cap)
     check(got, q, k, v, table, ln, 0.125, 0, ks, vs, cap, None)
+
+
+def paired(lens, Q, G, Hkv, page, seed, order="nhd"):
+    """An E4M3 cache with heads of 64 and a table wide enough for the form that takes
+    two heads side by side."""
+    q, k, v, table, ln, kc, vc, ks, vs = build(lens, Q, G * Hkv, Hkv, 64, page, E4M3, order,
+                                               seed=seed)
+    width = (1 << 19) // (Hkv * len(lens) * page) + 1
+    table = torch.cat([table, torch.full((len(lens), width), -1, dtype=torch.int32)], 1)
+    return q, k, v, table, ln, kc, vc, ks, vs
+
+
+PAIRS = [
+    # lens, Q, G, Hkv, page, window, order, softcap, bias
+    ([1], 1, 1, 2, 16, 0, "nhd", 30.0, False),
+    ([700], 1, 1, 16, 20, 0, "nhd", 0.0, True),
+    ([5000, 0, 1, 17, 333], 1, 4, 8, 16, 0, "nhd", 20.0, True),
+    ([5000, 0, 1, 17, 333], 2, 4, 8, 20, 0, "hnd", 0.0, True),
+    ([1000, 3, 777], 4, 2, 4, 4, 0, "wide", 5.0, False),
+    ([1000, 3, 777], 8, 1, 2, 64, 0, "beside", 0.0, True),
+    ([15, 16, 2049], 3, 1, 6, 48, 0, "nhd", 50.0, True),
+]
+
+
+@pytest.mark.parametrize("lens,Q,G,Hkv,page,window,order,cap,bias", PAIRS)
+def test_two_heads_side_by_side(lens, Q, G, Hkv, page, window, order, cap, bias):
+    say(f"[scored pairs] lens={lens} Q={Q} G={G} Hkv={Hkv} page={page} {order} cap={cap} "
+        f"bias={bias}")
+    q, k, v, table, ln, kc, vc, ks, vs = paired(lens, Q, G, Hkv, page, 16, order)
+    q = q * 4
+    slopes = slopes_of(G * Hkv) if bias else None
+    got = run(q, table, ln, kc, vc, ks, vs, E4M3, slopes, softcap=cap, window=window)
+    check(got, q, k, v, table, ln, 0.125, window, ks, vs, cap, slopes)
+    assert torch.equal(got, run(q, table, ln, kc, vc, ks, vs, E4M3, slopes, softcap=cap,
+                                window=window))
+
+
+@pytest.mark.parametrize("page", [16, 20])
+def test_side_by_side_with_a_window(page):
+    """A window of 2^16 keys, of 90000 and of 300."""
+    q, k, v, table, ln, kc, vc, ks, vs = build([90000, 300], 2, 8, 8, 64, page, E4M3, seed=17)
+    slopes = slopes_of(8) / 64
+    got = run(q, table, ln, kc, vc, ks, vs, E4M3, slopes, window=1 << 16)
+    check(got, q, k, v, table, ln, 0.125, 1 << 16, ks, vs, 0.0, slopes)
+
+
+@pytest.mark.parametrize("page", [16, 20])
+def test_side_by_side_unseen_and_nan_values(page):
+    """NaN behind each sequence and in pages that nobody has leave every row as it
+    was, bit for bit; a NaN value stays with the rows of its head that see it."""
+    lens, Q = [70, 700, 2], 2
+    q, k, v, table, ln, kc, vc, ks, vs = paired(lens, Q, 2, 4, page, 18)
+    slopes = slopes_of(8)
+    clean = run(q, table, ln, kc, vc, ks, vs, E4M3, slopes, softcap=9.0)
+    check(clean, q, k, v, table, ln, 0.125, 0, ks, vs, 9.0, slopes)
+    seen = torch.zeros(kc.shape[0], page, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        for j in range(n):
+            seen[table[b, j // page], j % page] = True
+    for c in (kc, vc):
+        c.view(torch.uint8)[(~seen).to(DEV)] = 0x7F
+    got = run(q, table, ln, kc, vc, ks, vs, E4M3, slopes, softcap=9.0)
+    assert torch.equal(got, clean)
+    vc.view(torch.uint8)[table[1, 699 // page], 699 % page, 1, 5] = 0xFF
+    got = run(q, table, ln, kc, vc, ks, vs, E4M3, slopes, softcap=9.0).view(3, 2, 4, 2, 64)
+    was = clean.view(3, 2, 4, 2, 64)
+    assert torch.isnan(got[1, 1, 1, :, 5]).all()
+    got[1, 1, 1] = was[1, 1, 1]
+    assert torch.equal(got, was)
