@@ -266,7 +266,9 @@ struct AttnPass {
   }
 
   // The scores' cap, z -> cap tanh(z / cap) (the scores come divided by it), and
-  // the bias slope * (key - the row's position).
+  // the bias slope * (key - the row's position). bf16, 8 sequences of two tokens,
+  // window 4096: 23.5 us without either, 26.2 capped, 25.9 biased, 26.5 both; NVFP4,
+  // 713 MB: 155, 161, 149 and 167 (in one run).
   __device__ __forceinline__ void modify(f32x4_t (&S)[RT][NU], const Cursor& cur) {
     if (a.softcap > 0.0f) {
       const float to = a.softcap * kLog2e;

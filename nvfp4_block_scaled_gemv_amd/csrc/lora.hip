@@ -7,7 +7,7 @@
 // that share it, and of y; for a few tokens the latency of loads that wait for
 // each other (ids, then weights).
 //
-// Rows are grouped on the device: a workgroup is launched for every row and
+// Rows are grouped on the device: workgroups are launched for every row and each
 // finds the rows of the same adapter among the ids (two ballots); it works if
 // its row is the first, 17th, .. of them and takes that one and the next 15,
 // which fill the 16 rows (columns) of the matrix instructions.
@@ -20,6 +20,13 @@
 //                outputs) makes all of t for itself, in the same order.
 // A's and x's products are exact in the matrix cores' fp32 sums. No atomics; a
 // row's bits do not depend on the other rows.
+//
+// Measured, K 4096: 1 token, 6144 outputs of three projections, rank 16 9.7 us (0.7
+// MB: a launch and five dependent loads); 48 rows of 38 adapters of ranks 16 to 64,
+// 24576 outputs 11 + 32 us, 105 MB and 128 in whole lines: B's rows come at 4 TB/s, as
+// each workgroup's wait for ids, sums and first loads is as long as its loads (more
+// wavefronts, loads of whole lines or two blocks of outputs changed it by 3 %). K
+// 12288, 128 rows of 16 adapters, rank 32, 4096 outputs 7.7 + 5.8 us for 24 MB.
 #include "elems.h"
 #include "internal.h"
 

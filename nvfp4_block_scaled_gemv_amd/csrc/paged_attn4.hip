@@ -4,9 +4,14 @@
 // pass and the join are those of the other caches (attn_wave.h).
 //
 // Bound: the bytes of K and V, 9/16 of one per element, and next to it the
-// vector ALU, which turns each element into a number: a tile of 32 keys of 128
-// is 4.6 KB, which the card reads in 390 clocks per CU, and some 270 vector
-// instructions of 4 clocks on each of four SIMDs.
+// vector ALU, which turns each element into a number. A tile of 64 rows of K and V
+// of 128 is 9.2 KB, of which the card reads one per CU in 780 clocks, one per SIMD
+// in 3100; a wavefront issues some 450 vector and 48 matrix instructions for it, 2300
+// clocks. So the long batch reads 5.0 TB/s (16 sequences of 20000 to 65536 keys,
+// 8 heads of 128, 713 MB: 132 us and 6.5 for the join, 99 at the rate of a plain
+// read) and the arithmetic of one wavefront has to run beside the loads of
+// another. Tiles of 64 rows (one page look-up, one maximum and one branch for each
+// 64, not 32) and V through LDS brought most of it: 165 -> 131 us.
 //
 // A code times its block's scale has 6 significant bits and lies between 2^-10
 // and 2688: it is exact in fp16 (and in bf16, which has no packed product). So
@@ -18,6 +23,8 @@
 //   element to 2^14 .. 2^15; fp16 then holds every element down to 2^-31 of that
 //   one whole, and the smaller ones to 2^-40 of it. The scores' factor
 //   takes the power back.
+// - V is loaded in whole rows, 16 bytes a lane, and goes through 9 KB of LDS of the
+//   wavefront's own, as the lanes need other stretches of it; so do both's scales.
 // - V^T wants pairs of keys where a byte holds a pair of dims: the nibbles of
 //   two keys' words change places first, 4 instructions for 16 elements, and
 //   each conversion gives one dim of two keys. The pair's two scales multiply it.
@@ -109,7 +116,7 @@ struct Attn4Wave
   float qs[RT];                                // scale of a row's scores
   f32x4_t O[RT][NV];
   uint32_t kr[NU][NJ], kb[SL];                 // K: codes of the lane's slots, scales as loaded
-  u32x4_t vr[VL];                          // V as loaded
+  u32x4_t vr[VL];                              // V as loaded
   uint32_t vl[SL];
   uint32_t vb[NU];                             // V's scales of the lane's slots: 4 to a word
   int64_t off[NO], boff[NO];                   // bytes, from place()
@@ -500,8 +507,8 @@ bool side_by_side(const AttnArgs& a) {
 }
 
 // The whole form takes tables of at most this many keys: two turns of its eight
-// wavefronts, or half of one where its workgroups are more than the CUs. Whole against split, us, 8 heads of 128, G 4: 1
-// sequence of 256 keys 7.7 / 12.1, 512 9.6 / 12.2, 1024 12.7 / 12.5; 4: 512 10.0 /
+// wavefronts, or half of one where its workgroups are more than the CUs. Whole
+// against split, us, 8 heads of 128, G 4: 1 sequence of 256 keys 7.7 / 12.1, 512 9.6 / 12.2, 1024 12.7 / 12.5; 4: 512 10.0 /
 // 12.4, 1024 14.0 / 13.5; 16: 512 12.4 / 14.9, 1024 16.4 / 18.8, 2048 22.9 / 21.8;
 // 64: 256 18.6 / 20.2, 512 26.6 / 21.8.
 int64_t whole_keys(const AttnArgs& a, int NHV) {
