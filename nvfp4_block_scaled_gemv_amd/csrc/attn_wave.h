@@ -27,8 +27,7 @@ constexpr int kMaxRuns = kCus * 4 * 2;
 struct AttnShape {
   int rows;        // G * Q
   int G;
-  int heads;       // key-value heads that a wavefront takes side by side
-  int NHV;         // heads as the wavefronts see them: Hkv / heads * row tiles
+  int NHV;         // heads as the wavefronts see them: Hkv / side by side * row tiles
   int groups;      // runs
   int page_shift;  // log2(page), or -1
   int cap;         // keys that a row of the table can name
@@ -519,16 +518,16 @@ __global__ __launch_bounds__(kWholeWaves * 64, 2) void k_attn_whole(const AttnAr
 // One workgroup per (sequence, head, row) of a sequence that several runs
 // share: the records' weights first, then groups of D / 4 threads add the
 // records in turn and meet in LDS.
-template <int D, int TILE>
+template <int D, int TILE, int HEADS>
 __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnShape sh) {
   constexpr int TD = D / 4, NG = 256 / TD;
   __shared__ float lds[NG][D + 4];
   __shared__ float lds_f[kMaxRuns];
   __shared__ float lds_red[2][4];
   const int b = blockIdx.x / sh.NHV, hv = blockIdx.x % sh.NHV, r = blockIdx.y;
-  const int all_heads = (int)a.Hkv / sh.heads;
-  const int rt_tile = hv / all_heads, hl = sh.heads == 1 ? 0 : r / sh.rows;
-  const int h = (hv - rt_tile * all_heads) * sh.heads + hl;
+  const int all_heads = (int)a.Hkv / HEADS;
+  const int rt_tile = hv / all_heads, hl = HEADS == 1 ? 0 : r / sh.rows;
+  const int h = (hv - rt_tile * all_heads) * HEADS + hl;
   const int rr = rt_tile * sh.slot_rows + r - hl * sh.rows;
   if (rr >= sh.rows) return;
   const Tiles<TILE> tiles(a, sh);
@@ -606,12 +605,11 @@ __global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnS
 // wavefronts), and where their records lie in the workspace.
 struct AttnLayout {
   size_t ml, o, total;
-  int RT, heads, slot_rows, NHV, groups;
+  int RT, slot_rows, NHV, groups;
 };
 AttnLayout attn_layout(int64_t rows, int64_t Hkv, int64_t D, int RT, int per_simd, int heads = 1) {
   AttnLayout L;
   L.RT = RT;
-  L.heads = heads;
   L.NHV = (int)(Hkv / heads * ((rows + L.RT * 16 - 1) / (L.RT * 16)));
   L.slot_rows = (int)(heads * (rows < L.RT * 16 ? rows : L.RT * 16));
   L.groups = kCus * 4 * per_simd / L.NHV;
@@ -639,7 +637,6 @@ AttnShape attn_shape(const AttnArgs& a, const AttnLayout& L) {
   AttnShape sh;
   sh.G = (int)(a.Hq / a.Hkv);
   sh.rows = sh.G * (int)a.Q;
-  sh.heads = L.heads;
   sh.NHV = L.NHV;
   sh.groups = L.groups;
   sh.cap = capacity(a);
@@ -676,7 +673,7 @@ hipError_t launch_forms(const AttnArgs& a, AttnShape sh, int64_t whole, hipStrea
                      a, sh);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || keys <= Wave::kTile) return e;   // a sequence of one tile is never shared
-  hipLaunchKernelGGL((k_attn_join<D, Wave::kTile>),
+  hipLaunchKernelGGL((k_attn_join<D, Wave::kTile, Wave::kHeads>),
                      dim3((uint32_t)(a.B * sh.NHV), (uint32_t)sh.slot_rows), dim3(256), 0, stream,
                      a, sh);
   return hipGetLastError();
