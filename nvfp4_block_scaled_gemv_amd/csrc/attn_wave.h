@@ -8,6 +8,7 @@
 #include <type_traits>
 
 #include "elems.h"
+#include "attn_cap.h"
 #include "attn_span.h"
 #include "internal.h"
 
@@ -130,23 +131,11 @@ __device__ __forceinline__ uint32_t perm_lo(uint32_t a, uint32_t b) {   // halve
 __device__ __forceinline__ uint32_t perm_hi(uint32_t a, uint32_t b) {   // halves 1 of a, b
   return __builtin_amdgcn_perm(b, a, 0x07060302u);
 }
-// tanh to 2^-21 of it. Up to 1.25 a quotient of its continued fraction, x (10395 +
-// 1260 s + 21 s^2) / (10395 + 4725 s + 210 s^2 + s^3) with s = x^2, off by 2^-27 at
-// most; beyond, 1 - 2 / (exp(2 x) + 1), which is 1 where the exponential overflows
-// (below, its rounding, 2^-24 of one, would show).
-constexpr float kTanhNear = 1.25f;
-__device__ __forceinline__ float tanh_near(float x) {
-  const float s = x * x;
-  const float n = fmaf(fmaf(s, 21.0f, 1260.0f), s, 10395.0f);
-  const float d = fmaf(fmaf(s + 210.0f, s, 4725.0f), s, 10395.0f);
-  return x * n * __builtin_amdgcn_rcpf(d);
-}
-__device__ __forceinline__ float tanh_any(float x) {
-  const float y = fabsf(x);
-  const float e = __builtin_amdgcn_exp2f(y * (2.0f * kLog2e));
-  const float far = fmaf(-2.0f, __builtin_amdgcn_rcpf(e + 1.0f), 1.0f);
-  return y <= kTanhNear ? tanh_near(x) : copysignf(far, x);
-}
+
+struct CapOps {
+  static __device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x); }
+  static __device__ __forceinline__ float exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+};
 
 // LDS is written and read by the lanes of one wavefront, in order: the compiler
 // has to keep that order across lanes too.
@@ -191,7 +180,7 @@ struct AttnPass {
   const int hl, col;                           // the lane's head from h on, and its row there
   int len_after;                               // of the sequence after the last cursor's
   int tok[RT];
-  const float c;                               // scale of the scores, log2 (cap: of tanh's argument)
+  const float c;                               // scale of the scores, log2
   float slope[RT];                             // of the row's head, log2 (MOD)
   float m[RT], l[RT];
   // Where a tile's keys lie. fetch() reads the page numbers, a tile ahead of
@@ -208,8 +197,7 @@ struct AttnPass {
         n(lane & 15), g(lane >> 4), h(h_), Q((int)a_.Q), G(sh_.G), row0(row0_),
         rows(sh_.rows - row0_ < RT * 16 ? sh_.rows - row0_ : RT * 16),
         hl(HEADS == 1 ? 0 : n / kCols), col(HEADS == 1 ? n : n % kCols),
-        c(MOD && a_.softcap > 0.0f ? a_.scale * k_scale / a_.softcap
-                                   : a_.scale * k_scale * kLog2e) {
+        c(a_.scale * k_scale * kLog2e) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int r = row0 + rt * 16 + col;
@@ -264,26 +252,26 @@ struct AttnPass {
     return (int64_t)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo);
   }
 
-  // The scores' cap, z -> cap tanh(z / cap) (the scores come divided by it), and
-  // the bias slope * (key - the row's position). bf16, 8 sequences of two tokens,
+  // The scores' cap, z -> cap tanh(z / cap), and the bias slope * (key - the row's
+  // position). bf16, 8 sequences of two tokens,
   // window 4096: 23.5 us without either, 26.2 capped, 25.9 biased, 26.5 both; NVFP4,
   // 713 MB: 155, 161, 149 and 167 (in one run).
   __device__ __forceinline__ void modify(f32x4_t (&S)[RT][NU], const Cursor& cur) {
     if (a.softcap > 0.0f) {
-      const float to = a.softcap * kLog2e;
+      const float cap = a.softcap * kLog2e, inv = CapOps::rcp(cap);
       float top = 0.0f;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int e = 0; e < 4 * NU; ++e) top = fmaxf(top, fabsf(S[rt][e >> 2][e & 3]));
       // most tiles of scores that a cap of tens is meant for hold none far out
-      const bool far = __any(top > kTanhNear);
+      const bool far = __any(top * inv > kCapNear);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int e = 0; e < 4 * NU; ++e) {
-          const float x = S[rt][e >> 2][e & 3];
-          S[rt][e >> 2][e & 3] = to * (far ? tanh_any(x) : tanh_near(x));
+          const float z = S[rt][e >> 2][e & 3];
+          S[rt][e >> 2][e & 3] = far ? capped<CapOps>(z, cap, inv) : capped_near<CapOps>(z, inv);
         }
     }
     if (a.slopes) {
