@@ -626,7 +626,7 @@ bool overlap(const void* p, size_t n, const CacheArrays& c) {
   return overlap(p, n, c.scale[0], 4) || overlap(p, n, c.scale[1], 4);
 }
 
-// What RopeArgs and AttnArgs hold of a cache.
+// What RopeArgs and AttnArgs (Attn4Args) hold of a cache.
 template <class Args>
 void put_cache(Args& a, const nvfp4_kv_cache& c) {
   a.cache_e4m3 = c.type == NVFP4_E4M3;
@@ -659,6 +659,23 @@ void put_cache(Args& a, const nvfp4_kv_cache4& c) {
   a.block_sh = c.scale_stride_head;
   a.k_scale = c.k_gscale;
   a.v_scale = c.v_gscale;
+}
+// A cache's attention: its arguments and launcher.
+nvfp4::AttnArgs attn_args(const nvfp4_kv_cache& c) {
+  nvfp4::AttnArgs a = {};
+  put_cache(a, c);
+  return a;
+}
+nvfp4::Attn4Args attn_args(const nvfp4_kv_cache4& c) {
+  nvfp4::Attn4Args a = {};
+  put_cache(a, c);
+  return a;
+}
+hipError_t launch_attn(const nvfp4::AttnArgs& a, hipStream_t stream) {
+  return nvfp4::launch_paged_attention(a, stream);
+}
+hipError_t launch_attn(const nvfp4::Attn4Args& a, hipStream_t stream) {
+  return nvfp4::launch_paged_attention4(a, stream);
 }
 nvfp4_status checks_of(const char* fn, const nvfp4_kv_cache& c) { return cache_checks(fn, c); }
 nvfp4_status checks_of(const char* fn, const nvfp4_kv_cache4& c) { return cache4_checks(fn, c); }
@@ -832,8 +849,7 @@ nvfp4_status attn_checked(const char* fn, const uint16_t* q, const Cache* cache,
     return fail(NVFP4_ERR_UNSUPPORTED, "%s: max_blocks=%lld or window=%lld is past 2^31 - 1", fn,
                 (long long)max_blocks, (long long)window);
   if (B == 0 || Q == 0 || Hq == 0) return NVFP4_OK;
-  nvfp4::AttnArgs a = {};
-  put_cache(a, *cache);
+  auto a = attn_args(*cache);
   a.B = B;
   a.Q = Q;
   a.Hq = Hq;
@@ -873,12 +889,12 @@ nvfp4_status attn_checked(const char* fn, const uint16_t* q, const Cache* cache,
   a.table = block_table;
   a.lens = seq_lens;
   a.scale = scale;
-  a.softcap = softcap;
+  a.cap = softcap * 1.4426950408889634f;
+  a.cap_inv = softcap > 0.0f ? 1.0f / a.cap : 0.0f;
   a.slopes = slopes;
   a.out = out;
   a.workspace = workspace;
-  return hip_result(a.cache_nvfp4 ? nvfp4::launch_paged_attention4(a, stream)
-                                  : nvfp4::launch_paged_attention(a, stream), fn);
+  return hip_result(launch_attn(a, stream), fn);
 }
 
 }  // namespace

@@ -37,10 +37,12 @@ struct AttnShape {
   float* o;        // [slots][slot_rows][D]
 };
 
+static_assert(sizeof(AttnArgs) + sizeof(AttnShape) <= 256, "four lines of arguments");
+
 typedef const __attribute__((address_space(4))) int32_t* const_i32;
 
 template <int TILE>
-__device__ __forceinline__ Span span_of(const AttnArgs& a, const AttnShape& sh, int len) {
+__device__ __forceinline__ Span span_of(const AttnCommon& a, const AttnShape& sh, int len) {
   return nvfp4::span_of<TILE>(len, sh.cap, a.Q, a.window);
 }
 
@@ -59,12 +61,12 @@ __device__ __forceinline__ int scan64(int v) {
 // The tiles of all sequences, by every wavefront for itself (all 64 lanes).
 template <int TILE>   // keys per tile
 struct Tiles {
-  const AttnArgs& a;
+  const AttnCommon& a;
   const AttnShape& sh;
   const int lane;
   int len, n, incl;   // of sequence `lane`, and the tiles up to it (of the first 64)
   int total;
-  __device__ __forceinline__ Tiles(const AttnArgs& a_, const AttnShape& sh_)
+  __device__ __forceinline__ Tiles(const AttnCommon& a_, const AttnShape& sh_)
       : a(a_), sh(sh_), lane(threadIdx.x & 63) {
     len = lane < (int)a.B ? a.lens[lane] : 0;
     n = lane < (int)a.B ? span_of<TILE>(a, sh, len).n : 0;
@@ -152,6 +154,14 @@ struct Cursor {
   int left;     // tiles of the sequence from it on
 };
 
+// The slopes of a lane's rows, log2: none where scores are neither capped nor biased.
+template <int RT, bool MOD>
+struct Slopes {
+  float slope[RT];
+};
+template <int RT>
+struct Slopes<RT, false> {};
+
 // A wavefront's pass over tiles of one head, for a class W derived from it that
 // holds K and V of a tile of TILE keys and the sums O; RT tiles of 16 rows share
 // it. Score e (of TILE / 4) of a lane is row rt * 16 + n and key W::key_of(e, g)
@@ -161,7 +171,7 @@ struct Cursor {
 // MOD: the scores are capped or biased. W::kStage: bytes of LDS that a wavefront
 // takes V through (0: none), in W::take_v().
 template <class W, int TILE, int RT, int RUN, bool MOD, int HEADS = 1, int NU_ = TILE / 16>
-struct AttnPass {
+struct AttnPass : Slopes<RT, MOD> {
   static_assert(HEADS == 1 || RT == 1, "heads side by side: one tile of rows");
   static constexpr int kTile = TILE;
   static constexpr int kHeads = HEADS;
@@ -172,16 +182,21 @@ struct AttnPass {
   typedef typename std::conditional<TILE == 64, uint64_t, uint32_t>::type Mask;   // bit per key
   static constexpr Mask kAll = ~(Mask)0;
 
-  const AttnArgs& a;
+  const AttnCommon& a;
   const AttnShape& sh;
   const const_i32 lens;
   const int lane, n, g;
   const int h, Q, G, row0, rows;
   const int hl, col;                           // the lane's head from h on, and its row there
+  const float c;                               // scale of the scores, log2
+  const int64_t head_off;                      // of head h in the cache
+  // What changes, after all that does not, and the slopes only where there are any:
+  // the order of the members decides how the compiler spends the registers. With
+  // the slopes always there and c among these, plain attention with two row tiles
+  // took 3 to 10 % longer (8 heads of 128, 20 rows, 64 sequences of 900 keys 66.6 us
+  // / 73.3; E4M3 heads of 64, 8 of 8192 36.0 / 38.5).
   int len_after;                               // of the sequence after the last cursor's
   int tok[RT];
-  const float c;                               // scale of the scores, log2
-  float slope[RT];                             // of the row's head, log2 (MOD)
   float m[RT], l[RT];
   // Where a tile's keys lie. fetch() reads the page numbers, a tile ahead of
   // resolve(), which turns them into places: of runs of keys inside one page
@@ -191,20 +206,21 @@ struct AttnPass {
   Mask ok;
 
   __device__ __forceinline__ W& self() { return *static_cast<W*>(this); }
-  __device__ __forceinline__ AttnPass(const AttnArgs& a_, const AttnShape& sh_, int h_, int row0_,
+  __device__ __forceinline__ AttnPass(const AttnCommon& a_, const AttnShape& sh_, int h_, int row0_,
                                       float k_scale)
       : a(a_), sh(sh_), lens((const_i32)(uintptr_t)a_.lens), lane(threadIdx.x & 63),
         n(lane & 15), g(lane >> 4), h(h_), Q((int)a_.Q), G(sh_.G), row0(row0_),
         rows(sh_.rows - row0_ < RT * 16 ? sh_.rows - row0_ : RT * 16),
         hl(HEADS == 1 ? 0 : n / kCols), col(HEADS == 1 ? n : n % kCols),
-        c(a_.scale * k_scale * kLog2e) {
+        c(a_.scale * k_scale * kLog2e),
+        head_off((int64_t)h_ * a_.sh) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const int r = row0 + rt * 16 + col;
       tok[rt] = r < sh.rows ? r / G : -1;
-      if (MOD)
-        slope[rt] = a.slopes && tok[rt] >= 0
-                        ? a.slopes[(h + hl) * G + r - tok[rt] * G] * kLog2e : 0.0f;
+      if constexpr (MOD)
+        this->slope[rt] = a.slopes && tok[rt] >= 0
+                              ? a.slopes[(h + hl) * G + r - tok[rt] * G] * kLog2e : 0.0f;
     }
   }
   __device__ __forceinline__ Cursor first_of(int b, int len, int idx) {
@@ -257,8 +273,12 @@ struct AttnPass {
   // window 4096: 23.5 us without either, 26.2 capped, 25.9 biased, 26.5 both; NVFP4,
   // 713 MB: 155, 161, 149 and 167 (in one run).
   __device__ __forceinline__ void modify(f32x4_t (&S)[RT][NU], const Cursor& cur) {
-    if (a.softcap > 0.0f) {
-      const float cap = a.softcap * kLog2e, inv = CapOps::rcp(cap);
+    if (a.cap > 0.0f) {
+      // Two row tiles over NVFP4 have no lane's register left for it (8 heads of 128, 20
+      // rows, pages of 20, 32773 keys: 66.3 us, 62.5 from the arguments), the other
+      // caches no scalar one (E4M3 heads of 64, 8 sequences of 8192 keys: 50.7 us from
+      // the arguments, 46.6).
+      const float inv = W::kCapInv ? a.cap_inv : CapOps::rcp(a.cap);
       float top = 0.0f;
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt)
@@ -271,7 +291,7 @@ struct AttnPass {
 #pragma unroll
         for (int e = 0; e < 4 * NU; ++e) {
           const float z = S[rt][e >> 2][e & 3];
-          S[rt][e >> 2][e & 3] = far ? capped<CapOps>(z, cap, inv) : capped_near<CapOps>(z, inv);
+          S[rt][e >> 2][e & 3] = far ? capped<CapOps>(z, a.cap, inv) : capped_near<CapOps>(z, inv);
         }
     }
     if (a.slopes) {
@@ -281,8 +301,19 @@ struct AttnPass {
 #pragma unroll
         for (int e = 0; e < 4 * NU; ++e)
           S[rt][e >> 2][e & 3] =
-              fmaf(slope[rt], (float)(from + W::key_of(e, g)), S[rt][e >> 2][e & 3]);
+              fmaf(this->slope[rt], (float)(from + W::key_of(e, g)), S[rt][e >> 2][e & 3]);
       }
+    }
+  }
+
+  // Values that no row sees may be anything: they become zero.
+  __device__ __forceinline__ void drop(const Cursor& cur, Mask ok_now, int t0, int t1) {
+    const int last = cur.len - Q + t1;
+    const int64_t firsts = a.window ? (int64_t)cur.len - Q + t0 - a.window + 1 : 0;
+#pragma unroll
+    for (int e = 0; e < 4 * NU; ++e) {
+      const int key = cur.key + W::key_of(e, g);
+      self().keep(e, key <= last && key >= firsts && ((ok_now >> W::key_of(e, g)) & 1u));
     }
   }
 
@@ -313,7 +344,7 @@ struct AttnPass {
       w.load_k(more);
       const Cursor nxt2 = after(nxt, step);
       fetch(nxt2);
-      if (MOD) modify(S, cur);
+      if constexpr (MOD) modify(S, cur);
       // every row sees the whole tile
       const int pos0 = cur.len - Q;
       const bool all = ok_now == kAll && cur.key + TILE - 1 <= pos0 &&
@@ -348,14 +379,7 @@ struct AttnPass {
       w.take_v();
       if (W::kStage) w.load_v(more);   // V is in LDS: its registers are free
       if (!all) {
-        // Values that no row sees may be anything: they become zero.
-        const int last = cur.len - Q + t1;
-        const int64_t firsts = a.window ? (int64_t)cur.len - Q + t0 - a.window + 1 : 0;
-#pragma unroll
-        for (int e = 0; e < 4 * NU; ++e) {
-          const int key = cur.key + W::key_of(e, g);
-          w.keep(e, key <= last && key >= firsts && ((ok_now >> W::key_of(e, g)) & 1u));
-        }
+        drop(cur, ok_now, t0, t1);
         if (HEADS == 1 && t1 > t0) w.settle(weightless);
       }
       // heads side by side: another head's values have weight 0 for a row, always
@@ -404,7 +428,7 @@ __device__ __forceinline__ int on_one_xcd(int b, int n) {
 
 // The split form: a wavefront per (run, head).
 template <class Wave>
-__global__ __launch_bounds__(256, Wave::kPerSimd) void k_attn_runs(const AttnArgs a,
+__global__ __launch_bounds__(256, Wave::kPerSimd) void k_attn_runs(const typename Wave::Args a,
                                                                    const AttnShape sh) {
   constexpr int D = Wave::kD, RT = Wave::kRT;
   __shared__ __align__(16) uint8_t stage[4][Wave::kStage ? Wave::kStage : 16];
@@ -453,7 +477,7 @@ __global__ __launch_bounds__(256, Wave::kPerSimd) void k_attn_runs(const AttnArg
 // The whole form: a workgroup per (sequence, head); its wavefronts take the
 // tiles in turn and meet in LDS.
 template <class Wave>
-__global__ __launch_bounds__(kWholeWaves * 64, 2) void k_attn_whole(const AttnArgs a,
+__global__ __launch_bounds__(kWholeWaves * 64, 2) void k_attn_whole(const typename Wave::Args a,
                                                                     const AttnShape sh) {
   constexpr int D = Wave::kD, RT = Wave::kRT;
   // a wavefront's sums, and before them the LDS of its pass
@@ -506,8 +530,8 @@ __global__ __launch_bounds__(kWholeWaves * 64, 2) void k_attn_whole(const AttnAr
 // One workgroup per (sequence, head, row) of a sequence that several runs
 // share: the records' weights first, then groups of D / 4 threads add the
 // records in turn and meet in LDS.
-template <int D, int TILE, int HEADS>
-__global__ __launch_bounds__(256) void k_attn_join(const AttnArgs a, const AttnShape sh) {
+template <int D, int TILE, int HEADS, class Args>
+__global__ __launch_bounds__(256) void k_attn_join(const Args a, const AttnShape sh) {
   constexpr int TD = D / 4, NG = 256 / TD;
   __shared__ float lds[NG][D + 4];
   __shared__ float lds_f[kMaxRuns];
@@ -610,18 +634,19 @@ AttnLayout attn_layout(int64_t rows, int64_t Hkv, int64_t D, int RT, int per_sim
 }
 
 // Keys that a row of the table can name (none where there is no page).
-int capacity(const AttnArgs& a) {
+int capacity(const AttnCommon& a) {
   const int64_t cap = a.num_blocks ? a.max_blocks * a.page : 0;
   return (int)(cap < 0x7FFFFFFF ? cap : 0x7FFFFFFF);
 }
 // Keys that a sequence reads at most: by its table row, or by its window
 // (which starts at most a tile early).
-int64_t most_keys(const AttnArgs& a) {
+int64_t most_keys(const AttnCommon& a) {
   const int64_t keys = capacity(a);
   return a.window && a.window + a.Q + 64 < keys ? a.window + a.Q + 64 : keys;
 }
 
-AttnShape attn_shape(const AttnArgs& a, const AttnLayout& L) {
+template <class Args>
+AttnShape attn_shape(const Args& a, const AttnLayout& L) {
   AttnShape sh;
   sh.G = (int)(a.Hq / a.Hkv);
   sh.rows = sh.G * (int)a.Q;
@@ -638,7 +663,8 @@ AttnShape attn_shape(const AttnArgs& a, const AttnLayout& L) {
 // The whole form for tables of at most `whole` keys, else the split form and,
 // where a sequence can be shared, the join.
 template <class Wave>
-hipError_t launch_forms(const AttnArgs& a, AttnShape sh, int64_t whole, hipStream_t stream) {
+hipError_t launch_forms(const typename Wave::Args& a, AttnShape sh, int64_t whole,
+                        hipStream_t stream) {
   constexpr int D = Wave::kD;
   const int64_t keys = most_keys(a);
   // no page at all: every sequence is empty
@@ -661,7 +687,7 @@ hipError_t launch_forms(const AttnArgs& a, AttnShape sh, int64_t whole, hipStrea
                      a, sh);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || keys <= Wave::kTile) return e;   // a sequence of one tile is never shared
-  hipLaunchKernelGGL((k_attn_join<D, Wave::kTile, Wave::kHeads>),
+  hipLaunchKernelGGL((k_attn_join<D, Wave::kTile, Wave::kHeads, typename Wave::Args>),
                      dim3((uint32_t)(a.B * sh.NHV), (uint32_t)sh.slot_rows), dim3(256), 0, stream,
                      a, sh);
   return hipGetLastError();

@@ -193,7 +193,7 @@ struct RopeArgs {
 hipError_t launch_rope_append(const RopeArgs& a, hipStream_t stream);
 
 // Attention of Q new tokens per sequence over a paged cache (paged_attn.hip).
-struct AttnArgs {
+struct AttnCommon {
   const uint16_t* q;                 // bf16 [B * Q, Hq, D]
   const void *k_cache, *v_cache;     // [num_blocks, page, Hkv, D], strided
   int64_t num_blocks, page, sb, st, sh;
@@ -201,25 +201,35 @@ struct AttnArgs {
   const int32_t* lens;               // [B]
   int64_t B, Q, Hq, Hkv, D, max_blocks, window;
   float scale;
-  float softcap;                     // > 0: scores z become softcap * tanh(z / softcap)
+  float cap;                         // > 0: scores z become cap tanh(z / cap), in log2 units
   const float* slopes;               // float [Hq] or NULL: + slopes[head] * (key - token's position)
   bool cache_e4m3, cache_nvfp4;
+  float cap_inv;                     // 1 / cap
   const float *k_scale, *v_scale;    // E4M3, NVFP4: float [1] each; bf16: NULL
-  // NVFP4: k_cache, v_cache hold the codes and sb, st, sh count bytes; the block
-  // scales, and their strides in bytes
-  const uint8_t *k_blocks, *v_blocks;
-  int64_t block_sb, block_st, block_sh;
+};
+// What a kernel gets. Apart, as each 64 bytes of a kernel's arguments cost it time:
+// with the block scales among the other caches' too (five lines of 64 bytes with
+// AttnShape, not four) 5 tokens on 32773 keys, 8 heads of 64, took 25.8 us, not 25.2.
+struct AttnArgs : AttnCommon {
   uint16_t* out;                     // bf16 [B * Q, Hq, D]
   void* workspace;
 };
+// NVFP4: k_cache, v_cache hold the codes and sb, st, sh count bytes; the block
+// scales, and their strides in bytes
+struct Attn4Args : AttnCommon {
+  const uint8_t *k_blocks, *v_blocks;
+  int64_t block_sb, block_st, block_sh;
+  uint16_t* out;
+  void* workspace;
+};
 // its tiles of keys and its launches stay within their 31 and 32 bits
-bool attn_fits(const AttnArgs& a);
+bool attn_fits(const AttnCommon& a);
 size_t attn_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv, int64_t D);
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream);
 // over an NVFP4 cache (paged_attn4.hip)
 int attn4_row_units(int64_t rows, int64_t Hkv, int64_t D);   // heads times row tiles
 size_t attn4_workspace_bytes(int64_t rows, int64_t Hkv, int64_t D);
-hipError_t launch_paged_attention4(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_paged_attention4(const Attn4Args& a, hipStream_t stream);
 
 // Low-rank adapters on the outputs of projections of one input (lora.hip).
 struct LoraSegment {

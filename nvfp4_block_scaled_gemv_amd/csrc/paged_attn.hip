@@ -110,13 +110,15 @@ struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD, HEADS>, TK / HEADS, RT,
                            HEADS, TK / 16> {
   using Pass = AttnPass<AttnWave, TK / HEADS, RT, PG ? 16 : 0, MOD, HEADS, TK / 16>;
   using Pass::a, Pass::sh, Pass::n, Pass::g, Pass::h, Pass::Q, Pass::G, Pass::row0, Pass::c,
-      Pass::tok, Pass::m, Pass::l, Pass::hl, Pass::col, Pass::NU, Pass::NO;
+      Pass::head_off, Pass::tok, Pass::m, Pass::l, Pass::hl, Pass::col, Pass::NU, Pass::NO;
   static_assert(HEADS == 1 || (FP8 && RT == 1 && D == 64), "any_nan, load_v");
   static constexpr bool kOthers = HEADS > 1;
+  using Args = AttnArgs;
   static constexpr int kD = D;
   static constexpr bool kScaled = FP8;
   static constexpr int kPerSimd = waves_per_simd(RT, D, FP8);
   static constexpr int kStage = 0;
+  static constexpr bool kCapInv = false;
   static constexpr int NP = TK / 32;           // products over the keys
   static constexpr int NJ = D / 32;            // products over the dims
   static constexpr int NV = D / 16;            // dims per lane of V
@@ -125,7 +127,6 @@ struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD, HEADS>, TK / HEADS, RT,
   static constexpr int kParts = 3;             // bf16 numbers that hold a probability
   typedef u32x4_t Weights[kParts][RT][NP];
 
-  const int64_t head_off;
   const uint32_t stb, shb, k_in, k_lane, v_dim, v_lane;   // bytes
   bf16x8_t qf[RT][NJ];
   f32x4_t O[RT][NV];
@@ -135,7 +136,7 @@ struct AttnWave : AttnPass<AttnWave<D, FP8, RT, PG, MOD, HEADS>, TK / HEADS, RT,
 
   __device__ __forceinline__ AttnWave(const AttnArgs& a_, const AttnShape& sh_, int h_, int row0_,
                                       float k_scale, uint8_t*)
-      : Pass(a_, sh_, h_, row0_, k_scale), head_off((int64_t)h_ * a_.sh),
+      : Pass(a_, sh_, h_, row0_, k_scale),
         stb((uint32_t)a_.st * ES), shb(HEADS == 1 ? 0u : (uint32_t)a_.sh * ES),
         k_in(head_of(n >> 2) * shb + (uint32_t)g * 16),
         k_lane((uint32_t)key_at(0, n >> 2, n & 3) * stb + k_in),
@@ -460,7 +461,7 @@ hipError_t launch_scored(const AttnArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-bool attn_fits(const AttnArgs& a) {
+bool attn_fits(const AttnCommon& a) {
   const int64_t rows = a.Hq / a.Hkv * a.Q;
   const int NHV = a.cache_nvfp4 ? attn4_row_units(rows, a.Hkv, a.D)
                                 : layout(rows, a.Hkv, a.D, a.cache_e4m3, a.page % 16 == 0).NHV;
@@ -484,7 +485,7 @@ size_t attn_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv, int64
 }
 
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream) {
-  return a.softcap > 0.0f || a.slopes ? launch_scored<true>(a, stream)
+  return a.cap > 0.0f || a.slopes ? launch_scored<true>(a, stream)
                                       : launch_scored<false>(a, stream);
 }
 

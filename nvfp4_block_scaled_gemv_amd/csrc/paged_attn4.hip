@@ -81,10 +81,12 @@ struct Attn4Wave
     : AttnPass<Attn4Wave<D, RT, RUN, MOD, HEADS>, 64 / HEADS, RT, RUN, MOD, HEADS> {
   using Pass = AttnPass<Attn4Wave, 64 / HEADS, RT, RUN, MOD, HEADS>;
   using Pass::a, Pass::sh, Pass::lane, Pass::n, Pass::g, Pass::h, Pass::Q, Pass::G, Pass::row0,
-      Pass::c, Pass::tok, Pass::m, Pass::l, Pass::hl, Pass::col, Pass::NO;
+      Pass::c, Pass::head_off, Pass::tok, Pass::m, Pass::l, Pass::hl, Pass::col, Pass::NO;
+  using Args = Attn4Args;
   static constexpr int kD = D;
   static constexpr bool kScaled = true;
   static constexpr bool kOthers = false;
+  static constexpr bool kCapInv = true;
   static constexpr int kPerSimd = waves_per_simd(D);
   static constexpr int NU = 4;                 // runs of 16 slots
   static constexpr int E = 16 / HEADS;         // scores that count per lane and row tile
@@ -106,7 +108,8 @@ struct Attn4Wave
   static constexpr int SL = D / 64;            // 4-byte loads of scales per lane and tile
   static constexpr int KS = 256 / kBlocks;     // slots of such a load
 
-  const int64_t head_off, head_boff;
+  const Attn4Args& more;                       // a, with the block scales
+  const int64_t head_boff;
   const uint32_t st, bst;
   const uint32_t sh1, bsh1;                    // from a head to the next
   const uint32_t k_in, v_in, b_in;             // the lane's bytes of K, V, scales in a load
@@ -121,9 +124,9 @@ struct Attn4Wave
   uint32_t vb[NU];                             // V's scales of the lane's slots: 4 to a word
   int64_t off[NO], boff[NO];                   // bytes, from place()
 
-  __device__ __forceinline__ Attn4Wave(const AttnArgs& a_, const AttnShape& sh_, int h_, int row0_,
-                                       float k_scale, uint8_t* stage)
-      : Pass(a_, sh_, h_, row0_, k_scale), head_off((int64_t)h_ * a_.sh),
+  __device__ __forceinline__ Attn4Wave(const Attn4Args& a_, const AttnShape& sh_, int h_,
+                                       int row0_, float k_scale, uint8_t* stage)
+      : Pass(a_, sh_, h_, row0_, k_scale), more(a_),
         head_boff((int64_t)h_ * a_.block_sh), st((uint32_t)a_.st), bst((uint32_t)a_.block_st),
         sh1((uint32_t)a_.sh), bsh1((uint32_t)a_.block_sh),
         k_in(in_load(n, st, sh1) + (uint32_t)g * (D / 8)),
@@ -189,7 +192,7 @@ struct Attn4Wave
     off[u] = (int64_t)((uint64_t)(uint32_t)id * (uint32_t)(a.sb >> 4)) * 16 +
              (int64_t)((uint64_t)(uint32_t)in * st) + head_off;
     boff[u] = alike ? off[u] >> 3
-                    : (int64_t)((uint64_t)(uint32_t)id * (uint32_t)(a.block_sb >> 2)) * 4 +
+                    : (int64_t)((uint64_t)(uint32_t)id * (uint32_t)(more.block_sb >> 2)) * 4 +
                           (int64_t)((uint64_t)(uint32_t)in * bst) + head_boff;
   }
   // The lane's e-th score (of E) is this key of the tile. Its slots of V and P
@@ -251,7 +254,7 @@ struct Attn4Wave
     load_k_run<1>(want);
     load_k_run<2>(want);
     load_k_run<3>(want);
-    load_scales<0>(a.k_blocks, want, kb);
+    load_scales<0>(more.k_blocks, want, kb);
   }
   // V: whole rows, 16 bytes a lane. Of each 16 slots the lanes take 0 4 8 12 1 5 ..
   // in turn, and so they lie in LDS: what the lanes' groups g read at once, slots
@@ -274,7 +277,7 @@ struct Attn4Wave
   }
   __device__ __forceinline__ void load_v(bool want) {
     load_v_from<0>(want);
-    load_scales<0>(a.v_blocks, want, vl);
+    load_scales<0>(more.v_blocks, want, vl);
   }
   // The scales of the tile's slots, 4 bytes a lane.
   template <int I>
@@ -502,7 +505,7 @@ AttnLayout layout(int64_t rows, int64_t Hkv, int64_t D, int heads) {
 // 41.9; 16 heads of 64, G 1, 16 of 20000 141 / 97. (Four heads: the long batch of
 // 713 MB 136 + 9.1 for the join against 131 + 6.8 with two and 161 + 6 with one.)
 // A load's bytes have to be counted in 32 bits.
-bool side_by_side(const AttnArgs& a) {
+bool side_by_side(const Attn4Args& a) {
   return a.B * most_keys(a) * a.Hkv >= 1 << 18 && a.sh < 1 << 28 && a.block_sh < 1 << 28;
 }
 
@@ -511,12 +514,12 @@ bool side_by_side(const AttnArgs& a) {
 // against split, us, 8 heads of 128, G 4: 1 sequence of 256 keys 7.7 / 12.1, 512 9.6 / 12.2, 1024 12.7 / 12.5; 4: 512 10.0 /
 // 12.4, 1024 14.0 / 13.5; 16: 512 12.4 / 14.9, 1024 16.4 / 18.8, 2048 22.9 / 21.8;
 // 64: 256 18.6 / 20.2, 512 26.6 / 21.8.
-int64_t whole_keys(const AttnArgs& a, int NHV) {
+int64_t whole_keys(const Attn4Args& a, int NHV) {
   return a.B * NHV > kCus ? 256 : 1024;
 }
 
 template <int D, int RT, bool MOD, int HEADS>
-hipError_t launch_run(const AttnArgs& a, const AttnShape& sh, hipStream_t stream) {
+hipError_t launch_run(const Attn4Args& a, const AttnShape& sh, hipStream_t stream) {
   const int64_t whole = HEADS == 1 ? whole_keys(a, sh.NHV) : 0;
   if (HEADS == 1 && a.page % 64 == 0)
     return launch_forms<Attn4Wave<D, RT, HEADS == 1 ? 64 : 16, MOD, HEADS>>(a, sh, whole, stream);
@@ -525,7 +528,7 @@ hipError_t launch_run(const AttnArgs& a, const AttnShape& sh, hipStream_t stream
 }
 
 template <int D, bool MOD>
-hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
+hipError_t launch_d(const Attn4Args& a, hipStream_t stream) {
   const int64_t rows = a.Hq / a.Hkv * a.Q;
   // (short tables take the whole form, which has one head a wavefront)
   const bool whole = D < 256 && most_keys(a) <= whole_keys(a, layout(rows, a.Hkv, D, 1).NHV);
@@ -539,7 +542,7 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
 }
 
 template <bool MOD>
-hipError_t launch_scored(const AttnArgs& a, hipStream_t stream) {
+hipError_t launch_scored(const Attn4Args& a, hipStream_t stream) {
   return a.D == 64    ? launch_d<64, MOD>(a, stream)
          : a.D == 128 ? launch_d<128, MOD>(a, stream)
                       : launch_d<256, MOD>(a, stream);
@@ -555,8 +558,8 @@ size_t attn4_workspace_bytes(int64_t rows, int64_t Hkv, int64_t D) {
   return one > more ? one : more;
 }
 
-hipError_t launch_paged_attention4(const AttnArgs& a, hipStream_t stream) {
-  return a.softcap > 0.0f || a.slopes ? launch_scored<true>(a, stream)
+hipError_t launch_paged_attention4(const Attn4Args& a, hipStream_t stream) {
+  return a.cap > 0.0f || a.slopes ? launch_scored<true>(a, stream)
                                       : launch_scored<false>(a, stream);
 }
 
