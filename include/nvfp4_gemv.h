@@ -686,7 +686,9 @@ nvfp4_status nvfp4_rope_append_nvfp4(const void* q, int64_t q_stride, const void
  * nvfp4_paged_attention_workspace_bytes -- device workspace that
  * nvfp4_paged_attention needs: the partial sums of the workgroups that share a
  * sequence and head. It does not grow with the lengths, and holds for
- * nvfp4_paged_attention_scored and nvfp4_paged_attention_nvfp4 too. 0 for sizes
+ * nvfp4_paged_attention_scored and nvfp4_paged_attention_nvfp4 too: it is the
+ * most that any of them uses. A call refuses less than it may use itself (plain
+ * attention over bf16 and E4M3: what it did before the others came). 0 for sizes
  * that the call refuses.
  */
 size_t nvfp4_paged_attention_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv,

@@ -660,7 +660,7 @@ void put_cache(Args& a, const nvfp4_kv_cache4& c) {
   a.k_scale = c.k_gscale;
   a.v_scale = c.v_gscale;
 }
-// A cache's attention: its arguments and launcher.
+// A cache's attention: its arguments, workspace and launcher.
 nvfp4::AttnArgs attn_args(const nvfp4_kv_cache& c) {
   nvfp4::AttnArgs a = {};
   put_cache(a, c);
@@ -670,6 +670,10 @@ nvfp4::Attn4Args attn_args(const nvfp4_kv_cache4& c) {
   nvfp4::Attn4Args a = {};
   put_cache(a, c);
   return a;
+}
+size_t attn_need(const nvfp4::AttnArgs& a) { return nvfp4::attn_workspace_need(a); }
+size_t attn_need(const nvfp4::Attn4Args& a) {
+  return nvfp4::attn4_workspace_bytes(a.Hq / a.Hkv * a.Q, a.Hkv, a.D);
 }
 hipError_t launch_attn(const nvfp4::AttnArgs& a, hipStream_t stream) {
   return nvfp4::launch_paged_attention(a, stream);
@@ -867,7 +871,10 @@ nvfp4_status attn_checked(const char* fn, const uint16_t* q, const Cache* cache,
     return fail(NVFP4_ERR_ALIGN,
                 "%s: q and out must be 16-byte, block_table, seq_lens and slopes 4-byte aligned",
                 fn);
-  const size_t need = nvfp4::attn_workspace_bytes(B, Q, Hq, Hkv, D);
+  a.cap = softcap * 1.4426950408889634f;
+  a.cap_inv = softcap > 0.0f ? 1.0f / a.cap : 0.0f;
+  a.slopes = slopes;
+  const size_t need = attn_need(a);
   if (!workspace || workspace_bytes < need)
     return fail(NVFP4_ERR_WORKSPACE, "%s: the workspace needs %zu bytes, %zu given", fn, need,
                 workspace ? workspace_bytes : (size_t)0);
@@ -889,9 +896,6 @@ nvfp4_status attn_checked(const char* fn, const uint16_t* q, const Cache* cache,
   a.table = block_table;
   a.lens = seq_lens;
   a.scale = scale;
-  a.cap = softcap * 1.4426950408889634f;
-  a.cap_inv = softcap > 0.0f ? 1.0f / a.cap : 0.0f;
-  a.slopes = slopes;
   a.out = out;
   a.workspace = workspace;
   return hip_result(launch_attn(a, stream), fn);

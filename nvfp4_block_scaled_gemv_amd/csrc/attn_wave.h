@@ -33,6 +33,7 @@ struct AttnShape {
   int page_shift;  // log2(page), or -1
   int cap;         // keys that a row of the table can name
   int slot_rows;   // rows of one partial record
+  int by_seq;      // records of runs' last parts: by a sequence, not by the run (part_at)
   float* ml;       // [slots][slot_rows][2]
   float* o;        // [slots][slot_rows][D]
 };
@@ -426,6 +427,16 @@ __device__ __forceinline__ int on_one_xcd(int b, int n) {
   return x * q + (x < r ? x : r) + (b >> 3);
 }
 
+// Run w's partial record of head hv: of its first part, or of its last. Two a run;
+// heads side by side have the last parts apart, as these may be counted by the
+// sequence b of the run's first tile (attn_layout): a run with a last part ends in a
+// later one, where the next run begins, so that no two such runs have the same.
+template <int HEADS>
+__device__ __forceinline__ int64_t part_at(const AttnShape& sh, int w, int hv, int last, int b) {
+  if (HEADS == 1) return (int64_t)(w * sh.NHV + hv) * 2 + last;
+  return (!last ? w : sh.groups + (sh.by_seq ? b : w)) * sh.NHV + hv;
+}
+
 // The split form: a wavefront per (run, head).
 template <class Wave>
 __global__ __launch_bounds__(256, Wave::kPerSimd) void k_attn_runs(const typename Wave::Args a,
@@ -446,7 +457,7 @@ __global__ __launch_bounds__(256, Wave::kPerSimd) void k_attn_runs(const typenam
   const float ks = Wave::kScaled ? *a.k_scale : 1.0f, vs = Wave::kScaled ? *a.v_scale : 1.0f;
   Wave wave(a, sh, h, rt_tile * (RT * 16), ks, stage[threadIdx.x >> 6]);
   bool from_start = s == before;
-  int64_t rec = (int64_t)(w * sh.NHV + hv) * 2 * sh.slot_rows;
+  int64_t rec = part_at<Wave::kHeads>(sh, w, hv, 0, b) * sh.slot_rows;
   wave.pass(wave.first_of(b, len, s - before), count, 1, [&](const Cursor& c) {
     const bool whole = from_start && c.left == 1;
 #pragma unroll
@@ -469,7 +480,7 @@ __global__ __launch_bounds__(256, Wave::kPerSimd) void k_attn_runs(const typenam
       }
     }
     // only a run's first and last parts can be records
-    rec = ((int64_t)(w * sh.NHV + hv) * 2 + 1) * sh.slot_rows;
+    rec = part_at<Wave::kHeads>(sh, w, hv, 1, b) * sh.slot_rows;
     from_start = true;
   });
 }
@@ -551,8 +562,12 @@ __global__ __launch_bounds__(256) void k_attn_join(const Args a, const AttnShape
   // a run that starts inside this sequence, or with it, has it as its first
   // part
   const int odd = runs.start(w0) == s0 ? 0 : 1;
+  int before, len, b0 = 0;
+  if (HEADS > 1 && odd && sh.by_seq) b0 = tiles.find(runs.start(w0), before, len);
   auto record = [&](int i) {
-    return (((int64_t)(w0 + i) * sh.NHV + hv) * 2 + (i == 0 ? odd : 0)) * sh.slot_rows + r;
+    const int last = i == 0 ? odd : 0;   // (one head: by lane, wider numbers at once)
+    if (HEADS == 1) return (((int64_t)(w0 + i) * sh.NHV + hv) * 2 + last) * sh.slot_rows + r;
+    return part_at<HEADS>(sh, w0 + i, hv, last, b0) * sh.slot_rows + r;
   };
   const int np = w1 - w0 + 1, wv = threadIdx.x >> 6;
   // the first records' values are on their way while the weights are made
@@ -614,10 +629,17 @@ __global__ __launch_bounds__(256) void k_attn_join(const Args a, const AttnShape
 }
 
 // The most runs per head (all heads' together fill the SIMDs with `per_simd`
-// wavefronts), and where their records lie in the workspace.
+// wavefronts), and where their records lie in the workspace: two a run. One pair of
+// heads side by side has as many runs as two heads have by themselves, of twice the
+// rows: its records are one a run and one a sequence, in what the two heads need (or
+// two of half the runs, where the sequences are more). B sequences cost B of 2048
+// runs (heads of 256: 1024). Against two records a run, us: NVFP4, heads of 64, pages
+// of 16, 48 sequences of 17 to 16384 keys the same, 64 of 8192 each, which 2048 runs
+// divide evenly, 31.7 / 29.5; heads of 256, 64 of 4000 to 8200 56.9 / 54.8.
 struct AttnLayout {
   size_t ml, o, total;
   int RT, slot_rows, NHV, groups;
+  bool one;        // a record a run
 };
 AttnLayout attn_layout(int64_t rows, int64_t Hkv, int64_t D, int RT, int per_simd, int heads = 1) {
   AttnLayout L;
@@ -626,12 +648,15 @@ AttnLayout attn_layout(int64_t rows, int64_t Hkv, int64_t D, int RT, int per_sim
   L.slot_rows = (int)(heads * (rows < L.RT * 16 ? rows : L.RT * 16));
   L.groups = kCus * 4 * per_simd / L.NHV;
   if (L.groups < 1) L.groups = 1;
-  const size_t slots = (size_t)2 * L.groups * L.NHV;
+  L.one = heads == 2 && L.NHV == 1;
+  const size_t slots = (size_t)(L.one ? 1 : 2) * L.groups * L.NHV;
   L.ml = 0;
   L.o = (slots * L.slot_rows * 2 * sizeof(float) + 255) & ~(size_t)255;
   L.total = (L.o + slots * L.slot_rows * (size_t)D * sizeof(float) + 255) & ~(size_t)255;
   return L;
 }
+
+bool scored(const AttnCommon& a) { return a.cap > 0.0f || a.slopes; }
 
 // Keys that a row of the table can name (none where there is no page).
 int capacity(const AttnCommon& a) {
@@ -651,7 +676,8 @@ AttnShape attn_shape(const Args& a, const AttnLayout& L) {
   sh.G = (int)(a.Hq / a.Hkv);
   sh.rows = sh.G * (int)a.Q;
   sh.NHV = L.NHV;
-  sh.groups = L.groups;
+  sh.by_seq = L.one && a.B <= L.groups / 2;
+  sh.groups = L.one ? L.groups - (sh.by_seq ? (int)a.B : L.groups / 2) : L.groups;
   sh.cap = capacity(a);
   sh.page_shift = (a.page & (a.page - 1)) == 0 ? __builtin_ctzll((uint64_t)a.page) : -1;
   sh.slot_rows = L.slot_rows;

@@ -224,7 +224,9 @@ struct Attn4Args : AttnCommon {
 };
 // its tiles of keys and its launches stay within their 31 and 32 bits
 bool attn_fits(const AttnCommon& a);
+// the workspace for any cache, and what this call's forms may use of it
 size_t attn_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv, int64_t D);
+size_t attn_workspace_need(const AttnArgs& a);
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream);
 // over an NVFP4 cache (paged_attn4.hip)
 int attn4_row_units(int64_t rows, int64_t Hkv, int64_t D);   // heads times row tiles

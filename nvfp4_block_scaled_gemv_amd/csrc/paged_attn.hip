@@ -484,9 +484,17 @@ size_t attn_workspace_bytes(int64_t B, int64_t Q, int64_t Hq, int64_t Hkv, int64
   return most;
 }
 
+size_t attn_workspace_need(const AttnArgs& a) {
+  const int64_t rows = a.Hq / a.Hkv * a.Q;
+  const bool pg = a.page % 16 == 0;
+  const size_t one = layout(rows, a.Hkv, a.D, a.cache_e4m3, pg).total;
+  if (!a.cache_e4m3 || !scored(a) || !pairs(rows, a.Hkv, a.D)) return one;
+  const size_t two = layout(rows, a.Hkv, a.D, true, pg, 2).total;
+  return one > two ? one : two;
+}
+
 hipError_t launch_paged_attention(const AttnArgs& a, hipStream_t stream) {
-  return a.cap > 0.0f || a.slopes ? launch_scored<true>(a, stream)
-                                      : launch_scored<false>(a, stream);
+  return scored(a) ? launch_scored<true>(a, stream) : launch_scored<false>(a, stream);
 }
 
 }  // namespace nvfp4

@@ -559,8 +559,7 @@ size_t attn4_workspace_bytes(int64_t rows, int64_t Hkv, int64_t D) {
 }
 
 hipError_t launch_paged_attention4(const Attn4Args& a, hipStream_t stream) {
-  return a.cap > 0.0f || a.slopes ? launch_scored<true>(a, stream)
-                                      : launch_scored<false>(a, stream);
+  return scored(a) ? launch_scored<true>(a, stream) : launch_scored<false>(a, stream);
 }
 
 }  // namespace nvfp4
