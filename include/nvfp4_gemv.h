@@ -775,7 +775,7 @@ nvfp4_status nvfp4_paged_attention_scored(const uint16_t* q, const nvfp4_kv_cach
  * row of q enters them times a power of two that takes its largest element to
  * 2^14 or more: elements down to 2^-31 of that one whole, others to within 2^-39
  * of it. Probabilities enter the product with V as the sum of two fp16: within
- * 2^-24 of each, or 2^-36 of the row's largest. Scores, maxima, sums and
+ * 2^-23 of each, or 2^-36 of the row's largest. Scores, maxima, sums and
  * probabilities are fp32. A NaN scale byte stands for 16 NaN elements.
  * Everything else as nvfp4_paged_attention.
  */

@@ -270,9 +270,9 @@ struct AttnPass : Slopes<RT, MOD> {
   }
 
   // The scores' cap, z -> cap tanh(z / cap), and the bias slope * (key - the row's
-  // position). bf16, 8 sequences of two tokens,
-  // window 4096: 23.5 us without either, 26.2 capped, 25.9 biased, 26.5 both; NVFP4,
-  // 713 MB: 155, 161, 149 and 167 (in one run).
+  // position). bf16, 8 sequences of two tokens, window 4096: 24.3 us without either,
+  // 24.5 capped, 24.3 biased, 24.8 both; NVFP4, 713 MB: 144, 157, 153 and 164 (in one
+  // run).
   __device__ __forceinline__ void modify(f32x4_t (&S)[RT][NU], const Cursor& cur) {
     if (a.cap > 0.0f) {
       // Two row tiles over NVFP4 have no lane's register left for it (8 heads of 128, 20
@@ -698,7 +698,7 @@ hipError_t launch_forms(const typename Wave::Args& a, AttnShape sh, int64_t whol
     return launch_fill_zero((float*)a.out, (size_t)(a.B * a.Q * a.Hq * D / 2), stream);
   // Heads of 256 have no whole form: eight wavefronts leave 256 registers each,
   // which two row tiles of 128 fill already (4 to 53 VGPRs spill in three of the
-  // four bf16 and E4M3 forms).
+  // four bf16 and E4M3 forms, 11 to 58 where scored, 8 to 111 in NVFP4's).
   if constexpr (D < 256 && Wave::kHeads == 1) {
     if (keys <= whole) {
       hipLaunchKernelGGL((k_attn_whole<Wave>), dim3((uint32_t)(a.B * sh.NHV)),

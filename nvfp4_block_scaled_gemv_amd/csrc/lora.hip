@@ -22,7 +22,7 @@
 // row's bits do not depend on the other rows.
 //
 // Measured, K 4096: 1 token, 6144 outputs of three projections, rank 16 9.7 us (0.7
-// MB: a launch and five dependent loads); 48 rows of 38 adapters of ranks 16 to 64,
+// MB: a launch and five dependent loads); 48 rows of 39 adapters of ranks 16 to 64,
 // 24576 outputs 11 + 32 us, 105 MB and 128 in whole lines: B's rows come at 4 TB/s, as
 // each workgroup's wait for ids, sums and first loads is as long as its loads (more
 // wavefronts, loads of whole lines or two blocks of outputs changed it by 3 %). K
@@ -42,7 +42,7 @@ constexpr int kMaxChunks = 16;
 // Outputs per workgroup of k_lora_up. One, two or four blocks of 256 (the next one's
 // loads before one's outputs are stored), both kernels, us: 16 sequences of 8 rows,
 // rank 32 13.9 / 16.5 / 16.0; 128 rows of as many adapters, 6144 outputs, rank 16 26.2 /
-// 25.2 / 23.8, of one adapter 13.0 / 14.0 / 16.2; 48 rows of 38 adapters of ranks 16
+// 25.2 / 23.8, of one adapter 13.0 / 14.0 / 16.2; 48 rows of 39 adapters of ranks 16
 // to 64, 24576 outputs 44.5 / 44.1 / 45.4.
 constexpr int kOuts = 256;
 constexpr int kAllOuts = 1024;     // and of k_lora_all
@@ -95,11 +95,18 @@ __device__ __forceinline__ Rows rows_of(const LoraArgs& a, int m, int (&list)[16
 // The row of a workgroup (M and more: none). From 16 rows on they start in the order
 // 0 8 16 .., 4 12 .., 2 10 .., 6 .., 1 .., 5 .., 3 .., 7 ..: where a request has
 // several rows, which are neighbours as a rule, those that begin a group start
-// early, and the workgroups that have nothing to do, of 1 us each, late. Rows in
-// turn against this, us: 16 sequences of 8 rows, K 12288, 4096 outputs, rank 32 22.9 /
-// 16.7 (the 16 adapters in turn over the rows 16.7 / 21.9); 128 rows of one adapter,
-// 6144 outputs 18.5 / 14.1, of as many 25.3 / 25.2; 48 rows of 38, 24576 outputs
-// 42.3 / 44.1.
+// early, and the workgroups that have nothing to do, of 1 us each, late. It is made
+// for groups of 2, 4 and 8 rows and more; those of 3 and 5, and adapters in turn over
+// the rows, may lose by it. Rows in turn against this, both kernels, us, groups of
+//                                       1     2     3     4     5     6     8     12    all
+//   K 12288, 4096 outputs, 128 rows  now 40.0  21.2  21.1  16.0  19.3  17.5  13.8  14.7  14.0
+//     rank 32                    in turn 37.7  29.4  21.1  22.8  19.2  20.0  19.3  18.0  18.5
+//                          48 rows  now 16.5  14.3  16.2  12.7  14.2  13.4  10.4  12.8  11.3
+//                                in turn 16.6  15.7  13.8  13.8  12.5  12.3  13.4  11.4  14.3
+//   K 4096, 6144 outputs, 128 rows  now 26.8  17.8  17.5  14.2  16.7  14.2  11.8  12.3  11.3
+//     rank 16                    in turn 25.7  21.9  17.4  17.0  15.9  16.2  15.7  14.3  15.6
+//   16 adapters in turn over 128 rows: 18.4 / 13.8 and 15.5 / 11.8 (now / in turn); groups of
+//   1 to 8 at random 19.2 / 20.4 and 16.3 / 18.3.
 __device__ __forceinline__ int row_of_block() {
   const int z = blockIdx.z;
   return blockIdx.y * gridDim.z + ((z & 1) * 4 + (z & 2) + (z >> 2));

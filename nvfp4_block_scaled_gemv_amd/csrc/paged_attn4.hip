@@ -7,11 +7,12 @@
 // vector ALU, which turns each element into a number. A tile of 64 rows of K and V
 // of 128 is 9.2 KB, of which the card reads one per CU in 780 clocks, one per SIMD
 // in 3100; a wavefront issues some 450 vector and 48 matrix instructions for it, 2300
-// clocks. So the long batch reads 5.0 TB/s (16 sequences of 20000 to 65536 keys,
-// 8 heads of 128, 713 MB: 132 us and 6.5 for the join, 99 at the rate of a plain
-// read) and the arithmetic of one wavefront has to run beside the loads of
-// another. Tiles of 64 rows (one page look-up, one maximum and one branch for each
-// 64, not 32) and V through LDS brought most of it: 165 -> 131 us.
+// clocks. So the long batch (16 sequences of 20000 to 65536 keys, 8 heads of 128, 713
+// MB) takes 131 to 191 us, by where its inputs lie in memory, 178 in the median, and 6
+// to 8 for the join: 5.4 to 3.7 TB/s, where a plain read takes 99. The arithmetic of
+// one wavefront has to run beside the loads of another. Tiles of 64 rows (one page
+// look-up, one maximum and one branch for each 64, not 32) and V through LDS brought
+// most of it: 165 -> 131 us on one set of inputs.
 //
 // A code times its block's scale has 6 significant bits and lies between 2^-10
 // and 2688: it is exact in fp16 (and in bf16, which has no packed product). So
@@ -21,16 +22,16 @@
 //   and their scales; two codes a conversion, two elements a packed product.
 // - Q: a row of bf16 is multiplied by a power of two that takes its largest
 //   element to 2^14 .. 2^15; fp16 then holds every element down to 2^-31 of that
-//   one whole, and the smaller ones to 2^-40 of it. The scores' factor
-//   takes the power back.
-// - V is loaded in whole rows, 16 bytes a lane, and goes through 9 KB of LDS of the
-//   wavefront's own, as the lanes need other stretches of it; so do both's scales.
+//   one whole, and the smaller ones to 2^-39 of it. The scores' factor takes the
+//   power back.
+// - V is loaded in whole rows, 16 bytes a lane, and goes through LDS of the wavefront's
+//   own (5 KB with both's scales at 128), as the lanes need other stretches of it.
 // - V^T wants pairs of keys where a byte holds a pair of dims: the nibbles of
 //   two keys' words change places first, 4 instructions for 16 elements, and
 //   each conversion gives one dim of two keys. The pair's two scales multiply it.
-// - P enters as the sum of two fp16, each rounded to nearest: 2^-24 of it at
-//   most is lost, or 2^-36 of the largest weight at small ones. The exponents
-//   are raised by 11 to use fp16's range.
+// - P enters as the sum of two fp16, each rounded to nearest: 2^-23 of it at most is
+//   lost (of what the first leaves 12 bits, the last of them set), or 2^-36 of the
+//   largest weight at small ones. The exponents are raised by 11 to use fp16's range.
 #include "attn_wave.h"
 
 namespace nvfp4 {
@@ -48,9 +49,13 @@ constexpr float kSlack = 4.0f;
 constexpr float kRaise = 11.0f;
 
 // Wavefronts per SIMD of the split form: the second one's arithmetic runs while
-// the first waits. Two against one, us: heads of 128, the long batch of 713 MB 161 /
-// 205; 20 rows (two tiles), 8 sequences of 20000 keys, 8 heads of 128 77 / 86, of
-// 64 53 / 67; heads of 256 160 / 151 (there the registers are too few: one).
+// the first waits. Two against one, us, 8 sequences of 20000 keys, 8 heads: of 128, 4
+// rows, pages of 16, 20 and 64 48 / 55, 54 / 70, 49 / 56; of 64, 20 rows (two tiles)
+// 59 / 73, 55 / 66, 52 / 64; of 256 160 / 151 (there the registers are too few: one).
+// Two tiles at heads of 128 fit into half of the registers only where a tile is
+// one page's (74 / 83 on pages of 64, 14 VGPRs spilled, 26 where scored): with a place for
+// each run of 16 or each key 91 to 106 spill, and one wavefront would be faster there
+// (pages of 16 190 / 90, of 20 216 / 106; capped 185 / 128, 210 / 143). Open.
 constexpr int waves_per_simd(int D) { return D < 256 ? 2 : 1; }
 static_assert(waves_per_simd(64) * kCus * 4 <= kMaxRuns, "the join's weights");
 
