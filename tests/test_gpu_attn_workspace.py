@@ -2,6 +2,8 @@
 as they are: two heads of an NVFP4 or E4M3 cache side by side, which are all of its
 heads or not, and fewer and more sequences than half of the runs; and plain attention
 in what it needed by itself."""
+import re
+
 import pytest
 import torch
 
@@ -92,3 +94,75 @@ def test_plain(ct, Q, G, Hkv, D, page):
     check_plain(got.cpu().double(), q, k, v, table, ln, D ** -0.5, 0, ks, vs)
     assert torch.all(raw[-GUARD:] == 0x5A)
     assert torch.equal(got, nv.paged_attention(*args, k_scale=a, v_scale=b))
+
+
+def demanded(call):
+    """The bytes that a call asks for when it gets too few."""
+    with pytest.raises(nv.Nvfp4Error) as e:
+        call(torch.empty(16, dtype=torch.uint8, device=DEV))
+    assert e.value.status == 5
+    return int(re.search(r"needs (\d+) bytes", str(e.value))[1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "bf16 scored", "e4m3 scored", "nvfp4"])
+@pytest.mark.parametrize("Q,G,Hkv,D,page", [(1, 4, 8, 128, 16), (1, 1, 16, 64, 20),
+                                            (1, 3, 2, 64, 16), (5, 4, 8, 128, 16),
+                                            (5, 4, 2, 256, 16), (3, 7, 3, 256, 20),
+                                            (20, 4, 1, 64, 64)])
+def test_what_a_call_demands_is_all_it_writes(kind, Q, G, Hkv, D, page):
+    """Exactly that many bytes, the ones behind them untouched, the same result as with
+    many more."""
+    lens = [6000, 17, 900, 0, 1]
+    g = gen(D + Q)
+    if kind == "nvfp4":
+        q, table, ln, parts = build4(lens, Q, G * Hkv, Hkv, D, page, seed=D)
+        cache = place4(parts, "nhd", DEV)
+    else:
+        q, _, _, table, ln, kc, vc, ks, vs = build(lens, Q, G * Hkv, Hkv, D, page,
+                                                   E4M3 if "e4m3" in kind else BF16, seed=D)
+        a, b = scales(kc.dtype, ks, vs)
+    table = widened(table, Hkv, page, 1 << 19)
+    args = (q.to(DEV), table.to(DEV), ln.to(DEV))
+    slopes = torch.rand(G * Hkv, generator=g).to(DEV)
+
+    def call(ws):
+        if kind == "nvfp4":
+            return nv.paged_attention_nvfp4(args[0], *cache, *args[1:], workspace=ws)
+        if "scored" in kind:
+            return nv.paged_attention_scored(args[0], kc, vc, *args[1:], softcap=20.0,
+                                             slopes=slopes, k_scale=a, v_scale=b, workspace=ws)
+        return nv.paged_attention(args[0], kc, vc, *args[1:], k_scale=a, v_scale=b, workspace=ws)
+    need = demanded(call)
+    most = nv.paged_attention_workspace_bytes(len(lens), Q, G * Hkv, Hkv, D)
+    assert need <= most
+    raw, ws = guarded(need)
+    got = call(ws)
+    torch.cuda.synchronize()
+    assert torch.all(raw[-GUARD:] == 0x5A)
+    assert torch.equal(got, call(torch.zeros(2 * most, dtype=torch.uint8, device=DEV)))
+    assert torch.isfinite(got.float()).all()
+
+
+def test_one_pair_of_heads_captured():
+    """A captured call over one pair of heads follows the lengths, its records counted by
+    sequences, with other work between the replays."""
+    q, table, ln, parts = build4([9000, 4000, 70, 3, 600], 1, 8, 2, 128, 16, seed=51)
+    table = widened(table, 2, 16, 1 << 18)
+    cache = place4(parts, "nhd", DEV)
+    dq, dt, dl = q.to(DEV), table.to(DEV), ln.to(DEV)
+    raw, ws = guarded(nv.paged_attention_workspace_bytes(5, 1, 8, 2, 128))
+    out = torch.empty_like(dq)
+    nv.paged_attention_nvfp4_into(dq, *cache, dt, dl, out, ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        nv.paged_attention_nvfp4_into(dq, *cache, dt, dl, out, ws)
+    for lens in ([9000, 4000, 70, 3, 600], [1, 0, 33, 3, 5], [9000, 1, 0, 0, 0],
+                 [100, 4000, 70, 2, 599], [8999, 3999, 69, 1, 1]):
+        dl.copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        want = nv.paged_attention_nvfp4(dq, *cache, dt, dl)
+        assert torch.equal(out, want), lens
+        four.check(out.cpu().double(), q, parts, table, torch.tensor(lens, dtype=torch.int32))
+    assert torch.all(raw[-GUARD:] == 0x5A)
