@@ -8,9 +8,10 @@
 // of 128 is 9.2 KB, of which the card reads one per CU in 780 clocks, one per SIMD
 // in 3100; a wavefront issues some 450 vector and 48 matrix instructions for it, 2300
 // clocks. So the long batch (16 sequences of 20000 to 65536 keys, 8 heads of 128, 713
-// MB) takes 131 to 191 us, by where its inputs lie in memory, 178 in the median, and 6
-// to 8 for the join: 5.4 to 3.7 TB/s, where a plain read takes 99. The arithmetic of
-// one wavefront has to run beside the loads of another. Tiles of 64 rows (one page
+// MB) takes 131 us in the first ten calls of a row, 150 to 200 in the next hundred and
+// 140 from then on, whatever the inputs, and 6 to 8 for the join: 5.1 TB/s, where a
+// plain read takes 99. The arithmetic of one wavefront has to run beside the loads of
+// another, at the rate that the card keeps under it. Tiles of 64 rows (one page
 // look-up, one maximum and one branch for each 64, not 32) and V through LDS brought
 // most of it: 165 -> 131 us on one set of inputs.
 //
